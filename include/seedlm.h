@@ -183,7 +183,8 @@ SEEDLM_API int seedlm_gemv_many(const seedlm_handle* handles, const void* const*
  * partials into the stream's scratch), _end adds the partials into y.  Called
  * with identical arguments on one stream they equal seedlm_gemv_many; the
  * split lets a caller time the two halves.  Between the two calls no other
- * gemv or gemm call may use that stream (it would reuse the scratch).
+ * gemv or gemm call, nor one of seedlm_serve.h, may use that stream (it would
+ * reuse the scratch).
  */
 SEEDLM_API int seedlm_gemv_many_begin(const seedlm_handle* handles, const void* const* x,
                                       void* const* y, int n, int batch, int x_dtype,
@@ -225,11 +226,12 @@ SEEDLM_API int seedlm_gemv_scratch_bytes(const seedlm_handle* handles, int n, in
                                          int x_dtype, int y_dtype, size_t* bytes);
 
 /*
- * seedlm_scratch_release -- free the gemv and gemm scratch of every stream on
- * every device (each device is synchronised first; graphs captured from earlier
- * calls must not be replayed afterwards).  Later calls allocate again.  Call
- * it after destroying a stream that gemv or gemm calls used, before a new
- * stream could take over its handle value.  Errors: SEEDLM_E_DEVICE.
+ * seedlm_scratch_release -- free the scratch (of gemv, gemm and seedlm_serve.h
+ * calls) of every stream on every device (each device is synchronised first;
+ * graphs captured from earlier calls must not be replayed afterwards).  Later
+ * calls allocate again.  Call it after destroying a stream that such calls
+ * used, before a new stream could take over its handle value.
+ * Errors: SEEDLM_E_DEVICE.
  */
 SEEDLM_API int seedlm_scratch_release(void);
 

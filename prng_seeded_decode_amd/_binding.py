@@ -56,6 +56,12 @@ EXPORTED = (
     "seedlm_encoder_create",
     "seedlm_encoder_destroy",
     "seedlm_encode",
+    "seedlm_cache_plan",
+    "seedlm_cache_append",
+    "seedlm_cache_attend",
+    "seedlm_cache_attend_scratch_bytes",
+    "seedlm_lora_many",
+    "seedlm_lora_scratch_bytes",
 )
 
 
@@ -119,6 +125,12 @@ def lib() -> ctypes.CDLL:
     L.seedlm_encoder_create.argtypes = [i32, i32, i32, i32, ctypes.POINTER(vp)]
     L.seedlm_encoder_destroy.argtypes = [vp]
     L.seedlm_encode.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
+    L.seedlm_cache_plan.argtypes = [vp, vp]
+    L.seedlm_cache_append.argtypes = [vp, vp]
+    L.seedlm_cache_attend.argtypes = [vp, vp]
+    L.seedlm_cache_attend_scratch_bytes.argtypes = [vp, ctypes.POINTER(sz)]
+    L.seedlm_lora_many.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, vp]
+    L.seedlm_lora_scratch_bytes.argtypes = [vp, i32, i64, i32, i32, ctypes.POINTER(sz)]
     for name in EXPORTED:
         if name != "seedlm_status_string":
             getattr(L, name).restype = i32

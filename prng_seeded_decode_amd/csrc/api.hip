@@ -62,30 +62,6 @@ std::mutex g_scratch_mu;
 std::vector<StreamScratch> g_scratch;
 std::vector<StreamScratch> g_retired;
 
-int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out) {
-  std::lock_guard<std::mutex> lock(g_scratch_mu);
-  StreamScratch* e = nullptr;
-  for (StreamScratch& c : g_scratch)
-    if (c.device == dev && c.stream == s) e = &c;
-  if (e && e->bytes >= bytes) {
-    *out = e->ptr;
-    return SEEDLM_OK;
-  }
-  size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
-  if (e && want < 2 * e->bytes) want = 2 * e->bytes;
-  void* p = nullptr;
-  if (hipMalloc(&p, want) != hipSuccess) return SEEDLM_E_NOMEM;
-  if (e) {
-    g_retired.push_back(*e);
-    e->ptr = p;
-    e->bytes = want;
-  } else {
-    g_scratch.push_back(StreamScratch{dev, s, p, want});
-  }
-  *out = p;
-  return SEEDLM_OK;
-}
-
 // ---- timing events of the main kernels (measurement only) ----
 struct TimingEvents {
   hipEvent_t start = nullptr, stop = nullptr;
@@ -341,6 +317,35 @@ int run_gemv(const seedlm_handle* hs, const void* const* x, void* const* y, int 
 }
 
 }  // namespace
+
+int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out) {
+  std::lock_guard<std::mutex> lock(g_scratch_mu);
+  StreamScratch* e = nullptr;
+  for (StreamScratch& c : g_scratch)
+    if (c.device == dev && c.stream == s) e = &c;
+  if (e && e->bytes >= bytes) {
+    *out = e->ptr;
+    return SEEDLM_OK;
+  }
+  size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
+  if (e && want < 2 * e->bytes) want = 2 * e->bytes;
+  void* p = nullptr;
+  if (hipMalloc(&p, want) != hipSuccess) return SEEDLM_E_NOMEM;
+  try {
+    if (e) {
+      g_retired.push_back(*e);
+      e->ptr = p;
+      e->bytes = want;
+    } else {
+      g_scratch.push_back(StreamScratch{dev, s, p, want});
+    }
+  } catch (const std::bad_alloc&) {
+    (void)hipFree(p);
+    return SEEDLM_E_NOMEM;
+  }
+  *out = p;
+  return SEEDLM_OK;
+}
 
 // The 2^16-entry table of extension bits b[16..47] (the TABLE variant keeps it
 // resident in L2 / the MALL instead of rebuilding the bits per block), one per

@@ -9,6 +9,7 @@
 
 #include "../../include/seedlm.h"
 #include "../../include/seedlm_bench.h"
+#include "../../include/seedlm_serve.h"
 
 namespace seedlm {
 
@@ -162,6 +163,22 @@ int launch_seed_table(int C, int P, int K, int Q, void* table, hipStream_t s);
 int launch_encode(int C, int P, int K, int Q, const void* table, const void* W, int64_t rows,
                   int64_t cols, void* seeds, int8_t* coeffs, int8_t* exps, float* err,
                   hipStream_t s);
+
+// Serving operators (seedlm_serve.h): launches of checked calls, with the
+// stream scratch that *_scratch_bytes asks for (NULL when that is 0).
+size_t cache_plan_scratch_bytes(const seedlm_cache_plan_args& a);
+int launch_cache_plan(const seedlm_cache_plan_args& a, int32_t* scratch, hipStream_t s);
+int launch_cache_append(const seedlm_cache_append_args& a, hipStream_t s);
+size_t cache_attend_scratch_bytes(const seedlm_cache_attend_args& a);
+int launch_cache_attend(const seedlm_cache_attend_args& a, void* scratch, hipStream_t s);
+constexpr int kLoraGroup = 8;  // sites of one pair of launches
+size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int xdt, int ydt);
+int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, const float* scales,
+                int64_t tokens, int adapters, int xdt, int ydt, float* scratch, hipStream_t s);
+
+// The library's scratch of a stream of device `dev`, at least `bytes` large
+// (calls on one stream share it in stream order).
+int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out);
 
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
