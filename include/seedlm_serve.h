@@ -206,7 +206,7 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  * Scratch: seedlm_lora_scratch_bytes, on the stream.  tokens = 0 and n = 0 are
  * no-ops.
  * Errors: SEEDLM_E_INVALID (null, range, a pointer not aligned to its type),
- * SEEDLM_E_UNSUPPORTED (dtype; rows, cols or tokens of 2^24 or more),
+ * SEEDLM_E_UNSUPPORTED (dtype; rows or cols of 2^24, tokens of 2^20 or more),
  * SEEDLM_E_NOMEM, SEEDLM_E_DEVICE.
  */
 typedef struct seedlm_lora_site {

@@ -130,7 +130,7 @@ int check_lora_sizes(const seedlm_lora_site* sites, int n, int64_t tokens, int x
       return SEEDLM_E_INVALID;
     if (s.rows >= kMost || s.cols >= kMost) return SEEDLM_E_UNSUPPORTED;
   }
-  return tokens >= kMost ? SEEDLM_E_UNSUPPORTED : SEEDLM_OK;
+  return tokens >= (int64_t)1 << 20 ? SEEDLM_E_UNSUPPORTED : SEEDLM_OK;
 }
 
 }  // namespace
