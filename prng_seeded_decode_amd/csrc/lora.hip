@@ -2,25 +2,23 @@
 // (seedlm_lora_many): y[t] = base[t] + scales[a] B_a (A_a x[t]), a = adapter[t],
 // for up to 8 sites (projections) in one pair of launches.
 //
-// First launch ("down"): h = A x, cut along the columns into chunks so that few
-// rows still fill the chip; chunk sums go to scratch as fp32
-// [site][chunk][token][rank].  Second launch ("up"): adds the chunks in order,
-// multiplies with B, scales, adds base and rounds once.
+// Two launches: "down" is h = A x, cut along the columns into chunks so that few
+// rows still fill the chip, its chunk sums going to scratch as fp32
+// [site][chunk][token][rank]; "up" adds the chunks in order, multiplies with B,
+// scales, adds base and rounds once.  Few rows with a small A take one launch, whose
+// workgroups each form h.
 //
-// Few rows (any types): a workgroup per row and chunk, lanes along the columns;
-// then a thread per output element.  The bytes of A and B bound it, once per row.
+// Few rows (any types, any sizes): a workgroup per row, chunk and 16 ranks, its lanes
+// along the columns, the 16 sums exchanged by halves across the wave; then a thread
+// per output.  The bytes of A and B, once per row, bound it.
 //
 // Many rows (fp16): v_mfma_f32_16x16x32_f16, with A (then B) as the first operand
 // and 16 rows as the second, so that a lane's results belong to one row:
-//   down  32 rows and up to 64 ranks per workgroup, its waves splitting a chunk
-//         of columns, added through LDS
-//   up    64 rows (a row per lane of the bookkeeping) and 64 outputs per wave; B
-//         is loaded once per adapter for all 64.  Operand row i of MFMA u is
-//         output 32 (u/2) + 8 (i/4) + 4 (u%2) + i%4, so that a lane's results of
-//         two MFMAs are 8 neighbouring outputs: 16-byte loads of base and stores
-//         of y.  h enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from
-//         the row's largest |h|), the 16 high and 16 low parts of 16 ranks filling
-//         the 32 products of one MFMA against the same 16 elements of B twice.
+//   down  32 rows and up to 64 ranks per workgroup, x and A staged through LDS
+//   up    16 rows and 128 outputs per wave and step; the sums turn over in LDS.  h
+//         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
+//         largest |h|), the 16 high and 16 low parts of 16 ranks filling the 32
+//         products of one MFMA against the same 16 elements of B twice.
 // A tile whose rows have several adapters takes them one after another and keeps
 // each result for its own rows only, so no adapter's values reach another's rows.
 // The bytes of x, base and y bound these.
@@ -33,11 +31,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kChunk = 1024;     // columns of a workgroup of the row kernels
+constexpr int kChunk = 8 * kThreads;  // columns of a workgroup of the row kernels
 constexpr int kDownRows = 32;    // rows, and ranks at most, of a down tile
 constexpr int kDownRanks = 64;
-constexpr int kUpRows = 64;      // rows and outputs of an up step
-constexpr int kUpOutputs = 64 * kWaves;
+constexpr int kDownStep = 256;   // columns staged at once
+constexpr int kUpRows = 16 * kWaves;  // rows of an up workgroup, 16 per wave
+constexpr int kUpStep = 128;          // outputs of a wave's step
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -94,56 +93,105 @@ __device__ void load8(const T* p, float (&v)[8]) {
   }
 }
 
-// h of one token and one chunk of columns: a wave takes the ranks in turn, its
-// lanes 8 neighbouring columns each (one by one where 16-byte loads do not fit).
+// Adds v[i] over the wave's lanes; lane l returns the sum of element l / 4 (halves
+// of the elements are exchanged at each of four steps, then two plain ones).
+__device__ float wave_sums16(float (&v)[16]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int step = 0; step < 4; ++step) {
+    constexpr int kHalf = 8;
+    const int n = kHalf >> step, d = 32 >> step;
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      if (i >= n) continue;
+      const float a = v[i], b = v[i + n];  // copies: a choice of elements is one by address
+      v[i] = (up ? b : a) + __shfl_xor(up ? a : b, d);
+    }
+  }
+  v[0] += __shfl_xor(v[0], 2);
+  return v[0] + __shfl_xor(v[0], 1);
+}
+
+// v[j] += A[j][c] x[c] for `ranks` <= 16 rows of A (past them the last one's again)
+// over the columns c0 + 8 tid + (0..7), c0 + 8 (tid + kBlock) + .., below c1 (one by
+// one where 16-byte loads do not fit).
+template <int kBlock, typename XT>
+__device__ void contract16(const XT* x, const __half* A, int cols, int ranks, bool wide, int c0,
+                           int c1, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  if (wide) {
+    for (int c = c0 + (int)threadIdx.x * 8; c < c1; c += kBlock * 8) {
+      half8 av[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        av[j] = *reinterpret_cast<const half8*>(A + (int64_t)min(j, ranks - 1) * cols + c);
+      float xv[8];
+      load8(x + c, xv);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j] = fmaf((float)av[j][i], xv[i], v[j]);
+    }
+  } else {
+    for (int c = c0 + (int)threadIdx.x; c < c1; c += kBlock) {
+      const float xc = (float)x[c];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        v[j] = fmaf(__half2float(A[(int64_t)min(j, ranks - 1) * cols + c]), xc, v[j]);
+    }
+  }
+}
+
+// 16 ranks of h of one token over one chunk of columns.
 template <typename XT>
 __global__ __launch_bounds__(kThreads) void lora_down_rows_kernel(const LoraArgs p) {
+  __shared__ float s_part[kWaves][16];
   const Site& s = site_of(p, false, blockIdx.x);
-  const int chunk = blockIdx.x - s.first_down;
+  const int rank_blocks = (s.rank + 15) / 16;
+  const int chunk = (blockIdx.x - s.first_down) / rank_blocks;
+  const int j0 = (blockIdx.x - s.first_down) % rank_blocks * 16;
+  const int ranks = min(16, s.rank - j0);
+  const int c0 = chunk * s.chunk_cols, c1 = min(s.cols, c0 + s.chunk_cols);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int t = blockIdx.y; t < p.tokens; t += gridDim.y) {
     const int a = p.adapter[t];
     if (a < 0 || a >= p.adapters) continue;
-    const int c0 = chunk * kChunk, c1 = min(s.cols, c0 + kChunk);
+    float v[16];
     const XT* x = static_cast<const XT*>(s.x) + (int64_t)t * s.cols;
-    const __half* A = s.A + (int64_t)a * s.rank * s.cols;
-    float* h = s.h + ((int64_t)chunk * p.tokens + t) * s.rank;
-    if (s.wide) {
-      constexpr int kSteps = kChunk / 512;
-      float xv[kSteps][8];
+    const __half* A = s.A + ((int64_t)a * s.rank + j0) * s.cols;
+    contract16<kThreads>(x, A, s.cols, ranks, s.wide, c0, c1, v);
+    const float sum = wave_sums16(v);
+    __syncthreads();  // s_part of the token before has been read
+    if ((lane & 3) == 0) s_part[wave][lane >> 2] = sum;
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < ranks) {
+      float h = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int c = c0 + k * 512 + lane * 8;
-        if (c < c1) load8(x + c, xv[k]);
-        else
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xv[k][i] = 0.f;
-      }
-      for (int j = wave; j < s.rank; j += kWaves) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const int c = c0 + k * 512 + lane * 8;
-          if (c < c1) {
-            float av[8];
-            load8(A + (int64_t)j * s.cols + c, av);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(av[i], xv[k][i], sum);
-          }
-        }
-        sum = wave_sum(sum);
-        if (lane == 0) h[j] = sum;
-      }
-    } else {
-      for (int j = wave; j < s.rank; j += kWaves) {
-        float sum = 0.f;
-        for (int c = c0 + lane; c < c1; c += 64)
-          sum = fmaf(__half2float(A[(int64_t)j * s.cols + c]), (float)x[c], sum);
-        sum = wave_sum(sum);
-        if (lane == 0) h[j] = sum;
-      }
+      for (int w = 0; w < kWaves; ++w) h += s_part[w][j];
+      s.h[((int64_t)chunk * p.tokens + t) * s.rank + j0 + j] = h;
     }
   }
+}
+
+// Row r of B_a times h (in LDS).
+__device__ float dot_b(const Site& s, int a, int r, const float* h) {
+  const __half* B = s.B + ((int64_t)a * s.rows + r) * s.rank;
+  float d = 0.f;
+  if (s.wide) {
+#pragma unroll 4
+    for (int j = 0; j < s.rank; j += 8) {
+      float bv[8];
+      load8(B + j, bv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d = fmaf(bv[i], h[j + i], d);
+    }
+  } else {
+    for (int j = 0; j < s.rank; ++j) d = fmaf(__half2float(B[j]), h[j], d);
+  }
+  return d;
 }
 
 // y of one token and kThreads rows, a row per thread.
@@ -169,21 +217,61 @@ __global__ __launch_bounds__(kThreads) void lora_up_rows_kernel(const LoraArgs p
     if (r >= s.rows) continue;
     const int64_t at = (int64_t)t * s.rows + r;
     float sum = (float)static_cast<const YT*>(s.base)[at];
-    if (has) {
-      const __half* B = s.B + ((int64_t)a * s.rows + r) * s.rank;
-      float d = 0.f;
-      if (s.wide) {
-        for (int j = 0; j < s.rank; j += 8) {
-          float bv[8];
-          load8(B + j, bv);
+    if (has) sum += dot_b(s, a, r, s_h);
+    static_cast<YT*>(s.y)[at] = (YT)sum;
+  }
+}
+
+// ---- fewest rows: one launch ----
+
+constexpr int kOneThreads = 1024;
+constexpr int kOneWaves = kOneThreads / 64;
+
+// y of one token and a block of outputs of one site, h included: every workgroup of
+// a token forms h again, its waves sharing the columns, which costs less than a
+// second launch while the repeated reads of A are few.
+template <typename XT, typename YT>
+__global__ __launch_bounds__(kOneThreads) void lora_one_kernel(const LoraArgs p, int blocks) {
+  __shared__ float s_part[kOneWaves][16];
+  __shared__ float s_h[SEEDLM_MAX_RANK];
+  // 8 tokens or more: a token's workgroups take one XCD (block number mod 8), whose
+  // L2 then serves the repeats
+  const int padded = (p.tokens + 7) / 8 * 8;
+  const bool near = p.tokens >= 8;
+  const int t = near ? blockIdx.x % padded : blockIdx.x / blocks;
+  const int block = near ? blockIdx.x / padded : blockIdx.x % blocks;
+  if (t >= p.tokens) return;
+  const Site& s = site_of(p, true, block);
+  const int a = p.adapter[t];
+  const bool has = a >= 0 && a < p.adapters;
+  if (!has && s.y == s.base) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (has) {
+    const XT* x = static_cast<const XT*>(s.x) + (int64_t)t * s.cols;
+    const __half* A = s.A + (int64_t)a * s.rank * s.cols;
+    for (int j0 = 0; j0 < s.rank; j0 += 16) {
+      const int ranks = min(16, s.rank - j0);
+      float v[16];
+      contract16<kOneThreads>(x, A + (int64_t)j0 * s.cols, s.cols, ranks, s.wide, 0, s.cols, v);
+      const float sum = wave_sums16(v);
+      __syncthreads();  // s_part has been read
+      if ((lane & 3) == 0) s_part[wave][lane >> 2] = sum;
+      __syncthreads();
+      if (tid < ranks) {
+        float h = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d = fmaf(bv[i], s_h[j + i], d);
-        }
-      } else {
-        for (int j = 0; j < s.rank; ++j) d = fmaf(__half2float(B[j]), s_h[j], d);
+        for (int w = 0; w < kOneWaves; ++w) h += s_part[w][tid];
+        s_h[j0 + tid] = h * p.scales[a];
       }
-      sum += d;
     }
+    __syncthreads();
+  }
+  const int first = (block - s.first_up) * s.up_outputs;
+  const int end = min(s.rows, first + s.up_outputs);
+  for (int r = first + tid; r < end; r += kOneThreads) {
+    const int64_t at = (int64_t)t * s.rows + r;
+    float sum = (float)static_cast<const YT*>(s.base)[at];
+    if (has) sum += dot_b(s, a, r, s_h);
     static_cast<YT*>(s.y)[at] = (YT)sum;
   }
 }
@@ -202,88 +290,107 @@ __device__ int adapter_of_lane(const LoraArgs& p, int t0, int n, int lane) {
   return a < p.adapters ? a : -1;
 }
 
-// h of kDownRows rows, RT * 16 ranks and one chunk.  Lane l supplies 8 columns
-// (8 (l/16) of each 32) of rank l%16 and of rows l%16 and 16 + l%16.
+// h of kDownRows rows, RT * 16 ranks and one chunk.  x and A pass through LDS, so
+// that a wave loads two rows of 512 bytes at once: read straight into operands, 16
+// rows of 64 bytes whose stride is a multiple of 4 KiB fall on few cache sets and
+// channels.  Wave w contracts rows 16 (w%2) + (0..15) over half w/2 of each step.
 template <int RT>
 __global__ __launch_bounds__(kThreads) void lora_down_tile_kernel(const LoraArgs p) {
-  __shared__ __align__(16) float s_h[kWaves][kDownRows][RT * 16 + 4];
+  constexpr int kRow = kDownStep + 8;  // halves between rows in LDS
+  constexpr int kRanks = RT * 16;
+  constexpr int kXLoads = kDownRows * kDownStep / 8 / kThreads;
+  constexpr int kALoads = kRanks * kDownStep / 8 / kThreads;
+  __shared__ __align__(16) uint16_t s_x[kDownRows * kRow];
+  __shared__ __align__(16) uint16_t s_a[kRanks * kRow];
+  __shared__ __align__(16) float s_h[kDownRows][kRanks + 4];  // of the second half
   const Site& s = site_of(p, false, blockIdx.x);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int m = lane & 15, g = lane >> 4;
-  constexpr int kDownSteps = 4;  // of 32 columns, requested together
   const int t0 = blockIdx.y * kDownRows;
-  const int rank_blocks = (s.rank + RT * 16 - 1) / (RT * 16);
+  const int rank_blocks = (s.rank + kRanks - 1) / kRanks;
   const int chunk = (blockIdx.x - s.first_down) / rank_blocks;
-  const int j0 = (blockIdx.x - s.first_down) % rank_blocks * (RT * 16);
-  // this wave's columns
-  const int quarter = s.chunk_cols / kWaves;
-  const int c0 = chunk * s.chunk_cols + wave * quarter;
-  const int c1 = min(s.cols, c0 + quarter);
+  const int j0 = (blockIdx.x - s.first_down) % rank_blocks * kRanks;
+  const int ranks = min(kRanks, s.rank - j0);  // a multiple of 8
+  const int c0 = chunk * s.chunk_cols, c1 = min(s.cols, c0 + s.chunk_cols);
   const int id = adapter_of_lane(p, t0, kDownRows, lane);
-  const __half* x[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    x[h] = static_cast<const __half*>(s.x) + (int64_t)min(t0 + h * 16 + m, p.tokens - 1) * s.cols;
+  // Thread tid stages 8 columns (tid % 32) of rows tid / 32 + 8 i.
+  const int col = tid % (kDownStep / 8) * 8, row = tid / (kDownStep / 8);
+  constexpr int kRowsAtOnce = kThreads / (kDownStep / 8);
+  const __half* x = static_cast<const __half*>(s.x);
   uint64_t todo = __ballot(id >= 0);
-  const uint64_t any = todo;
   while (todo) {
     const int a = __builtin_amdgcn_readlane(id, (int)__ffsll((unsigned long long)todo) - 1);
     const uint64_t own = __ballot(id == a);
     todo &= ~own;
-    floatx4 acc[2][RT];
+    const __half* A = s.A + ((int64_t)a * s.rank + j0) * s.cols;
+    v4u xv[kXLoads], av[kALoads];
+    auto request = [&](int c) {
+      const v4u z = {0, 0, 0, 0};
+      const bool in = c + col < c1;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[h][r] = floatx4{0.f, 0.f, 0.f, 0.f};
-    const __half* A[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      A[r] = s.A + ((int64_t)a * s.rank + min(j0 + r * 16 + m, s.rank - 1)) * s.cols;
-    for (int k = c0; k < c1; k += 32 * kDownSteps) {
-      v4u xv[kDownSteps][2], av[kDownSteps][RT];
-#pragma unroll
-      for (int u = 0; u < kDownSteps; ++u) {
-        const int c = k + 32 * u + 8 * g;
-        const bool in = c < c1;
-        const v4u z = {0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) xv[u][h] = in ? *reinterpret_cast<const v4u*>(x[h] + c) : z;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) av[u][r] = in ? *reinterpret_cast<const v4u*>(A[r] + c) : z;
+      for (int i = 0; i < kXLoads; ++i) {
+        const int t = min(t0 + row + kRowsAtOnce * i, p.tokens - 1);
+        xv[i] = in ? *reinterpret_cast<const v4u*>(x + (int64_t)t * s.cols + c + col) : z;
       }
 #pragma unroll
-      for (int u = 0; u < kDownSteps; ++u)
+      for (int i = 0; i < kALoads; ++i) {
+        const int j = min(row + kRowsAtOnce * i, ranks - 1);
+        av[i] = in ? *reinterpret_cast<const v4u*>(A + (int64_t)j * s.cols + c + col) : z;
+      }
+    };
+    floatx4 acc[RT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+    for (int r = 0; r < RT; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
+    request(c0);
+    for (int c = c0; c < c1; c += kDownStep) {
+      __syncthreads();  // the step before has been read
 #pragma unroll
-          for (int r = 0; r < RT; ++r) acc[h][r] = mfma(av[u][r], xv[u][h], acc[h][r]);
+      for (int i = 0; i < kXLoads; ++i)
+        *reinterpret_cast<v4u*>(&s_x[(row + kRowsAtOnce * i) * kRow + col]) = xv[i];
+#pragma unroll
+      for (int i = 0; i < kALoads; ++i)
+        *reinterpret_cast<v4u*>(&s_a[(row + kRowsAtOnce * i) * kRow + col]) = av[i];
+      if (c + kDownStep < c1) request(c + kDownStep);
+      __syncthreads();
+      const int k0 = (wave >> 1) * (kDownStep / 2) + g * 8;
+#pragma unroll
+      for (int k = 0; k < kDownStep / 2; k += 32) {
+        const v4u xk = *reinterpret_cast<const v4u*>(&s_x[((wave & 1) * 16 + m) * kRow + k0 + k]);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const v4u ak = *reinterpret_cast<const v4u*>(&s_a[(r * 16 + m) * kRow + k0 + k]);
+          acc[r] = mfma(ak, xk, acc[r]);
+        }
+      }
     }
+    // the second half's sums pass to the first's waves, which hold the same rows
+    const int t = (wave & 1) * 16 + m;
+    if (wave >= 2) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if ((own >> (h * 16 + m)) & 1) {
+      for (int r = 0; r < RT; ++r) *reinterpret_cast<floatx4*>(&s_h[t][r * 16 + g * 4]) = acc[r];
+    }
+    __syncthreads();
+    if (wave < 2 && ((own >> t) & 1)) {
+      float* h = s.h + ((int64_t)chunk * p.tokens + t0 + t) * s.rank + j0;
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-          *reinterpret_cast<floatx4*>(&s_h[wave][h * 16 + m][r * 16 + g * 4]) = acc[h][r];
+      for (int r = 0; r < RT; ++r) {
+        const int j = r * 16 + g * 4;
+        if (j < ranks)
+          *reinterpret_cast<floatx4*>(h + j) =
+              acc[r] + *reinterpret_cast<const floatx4*>(&s_h[t][j]);
       }
-  }
-  __syncthreads();
-  const int ranks = min(RT * 16, s.rank - j0);  // a multiple of 8
-  for (int e = threadIdx.x; e < kDownRows * RT * 4; e += kThreads) {
-    const int t = e / (RT * 4), j = e % (RT * 4) * 4;
-    if (!((any >> t) & 1) || j >= ranks) continue;
-    floatx4 sum = *reinterpret_cast<const floatx4*>(&s_h[0][t][j]);
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += *reinterpret_cast<const floatx4*>(&s_h[w][t][j]);
-    *reinterpret_cast<floatx4*>(s.h + ((int64_t)chunk * p.tokens + t0 + t) * s.rank + j0 + j) = sum;
+    }
   }
 }
 
-// y of kUpRows rows and s.up_outputs outputs.
-__global__ __launch_bounds__(kThreads, 2) void lora_up_tile_kernel(const LoraArgs p) {
+// y of kUpRows rows and s.up_outputs outputs; wave w has rows 16 w + (0..15).
+__global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p) {
   // h of the rows, each value as hi | lo << 16, ranks padded with zeros to
-  // sixteens; and the factor scales[a] * 2^e of each row
+  // sixteens; the factor scales[a] * 2^e of each row; and a wave's sums of a step,
+  // turned over so that base and y are read and written in runs of 256 bytes
   extern __shared__ __align__(16) uint32_t s_pair[];
   __shared__ float s_factor[kUpRows];
+  __shared__ __align__(16) float s_sum[kWaves][16][kUpStep + 4];
   const Site& s = site_of(p, true, blockIdx.x);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m = lane & 15, g = lane >> 4;
@@ -299,6 +406,7 @@ __global__ __launch_bounds__(kThreads, 2) void lora_up_tile_kernel(const LoraArg
       for (int j = part * 4; j < ranks; j += 16) {
         floatx4 sum = {0.f, 0.f, 0.f, 0.f};
         if (j < s.rank)
+#pragma unroll 4
           for (int c = 0; c < s.chunks; ++c)
             sum += *reinterpret_cast<const floatx4*>(
                 s.h + ((int64_t)c * p.tokens + t0 + t) * s.rank + j);
@@ -329,88 +437,87 @@ __global__ __launch_bounds__(kThreads, 2) void lora_up_tile_kernel(const LoraArg
     }
   }
   __syncthreads();
+  const int r0 = wave * 16;  // the wave's rows from here on
+  if (t0 + r0 >= p.tokens) return;
   const bool copies = s.y != s.base;
+  const uint32_t has = (uint32_t)(__ballot(id >= 0) >> r0) & 0xFFFF;
+  if (has == 0 && !copies) return;
   const uint32_t select = g < 2 ? 0x05040100u : 0x07060302u;  // high or low parts
-  const int o_end = min(s.rows, (int)(blockIdx.x - s.first_up + 1) * s.up_outputs);
-  for (int o0 = (blockIdx.x - s.first_up) * s.up_outputs + wave * 64; o0 < o_end; o0 += kUpOutputs) {
-    // base of rows 16 k + m, outputs o0 + 32 v + 8 g + (0..7)
-    v4u base[4][2];
+  const int o_begin = (blockIdx.x - s.first_up) * s.up_outputs;
+  const int o_end = min(s.rows, o_begin + s.up_outputs);
+  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows 4 i + l/16.
+  const __half* base = static_cast<const __half*>(s.base) + (int64_t)(t0 + r0) * s.rows + m * 8;
+  __half* y = static_cast<__half*>(s.y) + (int64_t)(t0 + r0) * s.rows + m * 8;
+  v4u bases[4];
+  auto request = [&](int o0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int t = min(t0 + 16 * k + m, p.tokens - 1), o = min(o0 + 32 * v + 8 * g, s.rows - 8);
-        base[k][v] = *reinterpret_cast<const v4u*>(static_cast<const __half*>(s.base) +
-                                                   (int64_t)t * s.rows + o);
-      }
-    __half* y = static_cast<__half*>(s.y);
-    uint64_t todo = __ballot(id >= 0);
-    if (copies) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = t0 + 16 * k + m;
-        if (t >= p.tokens || (todo >> (16 * k + m)) & 1) continue;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int o = o0 + 32 * v + 8 * g;
-          if (o < s.rows) *reinterpret_cast<v4u*>(y + (int64_t)t * s.rows + o) = base[k][v];
-        }
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens)
+        bases[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const v4u*>(base + (int64_t)(4 * i + g) * s.rows + o0));
+  };
+  request(o_begin);
+  for (int o0 = o_begin; o0 < o_end; o0 += kUpStep) {
+    uint32_t todo = has;
     while (todo) {
-      const int a = __builtin_amdgcn_readlane(id, (int)__ffsll((unsigned long long)todo) - 1);
-      const uint64_t own = __ballot(id == a);
+      const int a = __builtin_amdgcn_readlane(id, r0 + __ffs(todo) - 1);
+      const uint32_t own = (uint32_t)(__ballot(id == a) >> r0) & 0xFFFF;
       todo &= ~own;
-      const __half* B[4];
+      floatx4 acc[kUpStep / 16];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int o = o0 + 32 * (u >> 1) + 8 * (m >> 2) + 4 * (u & 1) + (m & 3);
-        B[u] = s.B + ((int64_t)a * s.rows + min(o, s.rows - 1)) * s.rank + (g & 1) * 8;
-      }
-      floatx4 acc[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[k][u] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < kUpStep / 16; ++u) acc[u] = floatx4{0.f, 0.f, 0.f, 0.f};
+      const __half* B = s.B + (int64_t)a * s.rows * s.rank + (g & 1) * 8;
       for (int j = 0; j < ranks; j += 16) {
-        v4u bv[4];
+        v4u bv[kUpStep / 16];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kUpStep / 16; ++u) {
+          const int o = min(o0 + 16 * u + m, s.rows - 1);
           bv[u] = v4u{0, 0, 0, 0};
-          if (j + (g & 1) * 8 < s.rank) bv[u] = *reinterpret_cast<const v4u*>(B[u] + j);
+          if (j + (g & 1) * 8 < s.rank)
+            bv[u] = *reinterpret_cast<const v4u*>(B + (int64_t)o * s.rank + j);
         }
+        const uint32_t* pair = &s_pair[(r0 + m) * stride + j + (g & 1) * 8];
+        const v4u p0 = *reinterpret_cast<const v4u*>(pair);
+        const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
+        const v4u hv = {__builtin_amdgcn_perm(p0[1], p0[0], select),
+                        __builtin_amdgcn_perm(p0[3], p0[2], select),
+                        __builtin_amdgcn_perm(p1[1], p1[0], select),
+                        __builtin_amdgcn_perm(p1[3], p1[2], select)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (((own >> (16 * k)) & 0xFFFF) == 0) continue;
-          const uint32_t* pair = &s_pair[(16 * k + m) * stride + j + (g & 1) * 8];
-          const v4u p0 = *reinterpret_cast<const v4u*>(pair);
-          const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
-          const v4u hv = {__builtin_amdgcn_perm(p0[1], p0[0], select),
-                          __builtin_amdgcn_perm(p0[3], p0[2], select),
-                          __builtin_amdgcn_perm(p1[1], p1[0], select),
-                          __builtin_amdgcn_perm(p1[3], p1[2], select)};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[k][u] = mfma(bv[u], hv, acc[k][u]);
-        }
+        for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], hv, acc[u]);
       }
+      if ((own >> m) & 1) {
+        const float f = s_factor[r0 + m];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (!((own >> (16 * k + m)) & 1)) continue;
-        const float f = s_factor[16 * k + m];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int o = o0 + 32 * v + 8 * g;
-          if (o >= s.rows) continue;
-          const __half* b = reinterpret_cast<const __half*>(&base[k][v]);
-          v4u out;
-          __half* q = reinterpret_cast<__half*>(&out);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            q[i] = __float2half_rn(fmaf(f, acc[k][2 * v + (i >> 2)][i & 3], __half2float(b[i])));
-          *reinterpret_cast<v4u*>(y + (int64_t)(t0 + 16 * k + m) * s.rows + o) = out;
-        }
+        for (int u = 0; u < kUpStep / 16; ++u)
+          *reinterpret_cast<floatx4*>(&s_sum[wave][m][16 * u + 4 * g]) = f * acc[u];
       }
     }
+    // the wave's own part of s_sum: its LDS accesses stay in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    v4u out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[i] = bases[i];
+      if (!((has >> (4 * i + g)) & 1)) continue;
+      const float* sum = &s_sum[wave][4 * i + g][m * 8];
+      const floatx4 lo = *reinterpret_cast<const floatx4*>(sum);
+      const floatx4 hi = *reinterpret_cast<const floatx4*>(sum + 4);
+      const __half* b = reinterpret_cast<const __half*>(&bases[i]);
+      __half* q = reinterpret_cast<__half*>(&out[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        q[k] = __float2half_rn(__half2float(b[k]) + (k < 4 ? lo[k & 3] : hi[k & 3]));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (o0 + kUpStep < o_end) request(o0 + kUpStep);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens &&
+          (copies || (has >> (4 * i + g)) & 1))
+        *reinterpret_cast<v4u*>(y + (int64_t)(4 * i + g) * s.rows + o0) = out[i];
   }
 }
 
@@ -423,29 +530,61 @@ bool wide_site(const seedlm_lora_site& s) {
   return s.cols % 8 == 0 && s.rank % 8 == 0 && aligned16(s.x) && aligned16(s.A) && aligned16(s.B);
 }
 
-// Rows from which a call runs on the matrix cores.
-constexpr int64_t kTileTokens = 33;
+// How the sites [0, n) of one group run.
+enum Kind { kOne, kRows, kTiles };
 
-// Whether the sites [0, n) of one pair of launches run on the matrix cores.
-bool tiles(const seedlm_lora_site* s, int n, int64_t tokens, int xdt, int ydt) {
-  if (tokens < kTileTokens || xdt != SEEDLM_F16 || ydt != SEEDLM_F16) return false;
-  for (int i = 0; i < n; ++i)
-    if (!wide_site(s[i]) || s[i].rows % 8 != 0 || !aligned16(s[i].base) || !aligned16(s[i].y))
-      return false;
-  return true;
+// Tiles need rows enough to fill them and products enough to repay their set-up.
+// GPU time of a call, tiles against rows, 8 requests of one adapter each: q, k and v
+// of a 70B layer at rank 16 14.1 and 12.1 us at 64 rows, 11.4 and 21 at 128; gate and
+// up of an 8B layer at rank 64 31 and 41 us at 64, 28 and 76 at 128; 512 x 512 at rank
+// 16 (17 MB at 512 rows) 8.0 and 6.9 at 512.  Rows that alternate among 16 adapters
+// cost the tiles more: 42 against 12 us for the first at 64 rows, 67 and 66 at 512.
+constexpr int64_t kTileTokens = 64;
+constexpr int64_t kTileBytes = 64 << 20;  // A and B, once per row
+// One launch pays while A is small for a workgroup to read whole and the workgroups
+// are at most the compute units (every one reads A).  One launch against two: q, k
+// and v of a 70B layer at rank 16 7.2 and 7.8 us at 16 rows, 9.0 and 12.0 at 64; gate
+// and up of an 8B layer 5.7 and 6.5 at 1, 7.8 and 9.9 at 32 (256 workgroups), 13.8
+// and 13.5 at 64; 512 x 512 4.8 and 5.8 at 1; 8192 x 28672 10.8 and 8.5; at rank 32 (two
+// turns) 4096 x 11008 11.9 and 7.9.
+constexpr int64_t kOneBytes = 256 << 10;  // of one adapter's A
+constexpr int kOneRank = 16;
+
+// Outputs of a workgroup of lora_one_kernel: a row per thread, or up to four where
+// there are more workgroups than compute units; *workgroups gets their number.
+int one_outputs(const seedlm_lora_site* s, int n, int64_t tokens, int64_t* workgroups) {
+  for (int per = kOneThreads;; per *= 2) {
+    *workgroups = 0;
+    for (int i = 0; i < n; ++i) *workgroups += (s[i].rows + per - 1) / per * tokens;
+    if (*workgroups <= device_cu_count() || per == 4 * kOneThreads) return per;
+  }
 }
 
-// Column chunks of a site of an n-site group: 1024 columns each for the row
-// kernels; for the tiles as few as give two workgroups per compute unit, of at
+Kind kind_of(const seedlm_lora_site* s, int n, int64_t tokens, int xdt, int ydt) {
+  int64_t bytes = 0, workgroups = 0;
+  bool one = true, tile = tokens >= kTileTokens && xdt == SEEDLM_F16 && ydt == SEEDLM_F16;
+  for (int i = 0; i < n; ++i) {
+    bytes += tokens * s[i].rank * (s[i].rows + s[i].cols) * 2;
+    one = one && s[i].rank <= kOneRank && s[i].rank * s[i].cols * 2 <= kOneBytes;
+    tile = tile && wide_site(s[i]) && s[i].rows % 8 == 0 && aligned16(s[i].base) &&
+           aligned16(s[i].y);
+  }
+  (void)one_outputs(s, n, tokens, &workgroups);
+  if (one && workgroups <= device_cu_count()) return kOne;
+  return tile && bytes >= kTileBytes ? kTiles : kRows;
+}
+
+// Column chunks of a site of an n-site group: kChunk columns each for the row
+// kernels; for the tiles as few as give four workgroups per compute unit, of at
 // least 512 columns.
-int chunk_cols_of(const seedlm_lora_site& s, int n, int64_t tokens, bool tile) {
-  if (!tile) return kChunk;
+int chunk_cols_of(const seedlm_lora_site& s, int n, int64_t tokens, Kind kind) {
+  if (kind != kTiles) return kChunk;
   const int64_t across = (tokens + kDownRows - 1) / kDownRows * n;
-  int64_t chunks = (2 * device_cu_count() + across - 1) / across;
+  int64_t chunks = (4 * device_cu_count() + across - 1) / across;
   const int64_t most = (s.cols + 511) / 512;
   if (chunks > most) chunks = most;
   const int64_t cols = (s.cols + chunks - 1) / chunks;
-  return (int)((cols + 127) / 128 * 128);
+  return (int)((cols + kDownStep - 1) / kDownStep * kDownStep);
 }
 
 size_t site_floats(const seedlm_lora_site& s, int chunk_cols, int64_t tokens) {
@@ -453,7 +592,23 @@ size_t site_floats(const seedlm_lora_site& s, int chunk_cols, int64_t tokens) {
   return (size_t)((chunks * tokens * s.rank + 63) / 64 * 64);
 }
 
+// Outputs of an up workgroup: as many steps as leave four workgroups per compute
+// unit, at most 4 (every workgroup forms the rows' h again).
+int up_outputs_of(const seedlm_lora_site& s, int n, int64_t tokens) {
+  const int64_t steps = (s.rows + kUpStep - 1) / kUpStep;
+  const int64_t all = (tokens + kUpRows - 1) / kUpRows * steps * n;
+  const int64_t each = all / (4 * device_cu_count());
+  return (int)(each < 1 ? 1 : (each > 4 ? 4 : each)) * kUpStep;
+}
+
 int group_size(int n, int i) { return n - i < kLoraGroup ? n - i : kLoraGroup; }
+
+template <typename XT, typename YT>
+void run_one(const LoraArgs& p, int blocks, hipStream_t s) {
+  const int rows = p.tokens >= 8 ? (p.tokens + 7) / 8 * 8 : p.tokens;
+  hipLaunchKernelGGL((lora_one_kernel<XT, YT>), dim3(rows * blocks), dim3(kOneThreads), 0, s, p,
+                     blocks);
+}
 
 template <typename XT, typename YT>
 void run_rows(const LoraArgs& p, int down, int up, hipStream_t s) {
@@ -469,10 +624,10 @@ size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, 
   size_t most = 0;
   for (int i = 0; i < n; i += kLoraGroup) {
     const int k = group_size(n, i);
-    const bool tile = tiles(sites + i, k, tokens, xdt, ydt);
+    const Kind kind = kind_of(sites + i, k, tokens, xdt, ydt);
     size_t floats = 0;
-    for (int j = i; j < i + k; ++j)
-      floats += site_floats(sites[j], chunk_cols_of(sites[j], k, tokens, tile), tokens);
+    for (int j = i; j < i + k && kind != kOne; ++j)
+      floats += site_floats(sites[j], chunk_cols_of(sites[j], k, tokens, kind), tokens);
     if (floats > most) most = floats;
   }
   return most * sizeof(float);
@@ -487,12 +642,16 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
     p.scales = scales;
     p.tokens = (int)tokens;
     p.adapters = adapters;
-    const bool tile = tiles(sites + i, p.n, tokens, xdt, ydt);
+    const Kind kind = kind_of(sites + i, p.n, tokens, xdt, ydt);
+    const bool tile = kind == kTiles;
     float* h = scratch;
     int top_rank = 0;
     for (int k = 0; k < p.n; ++k)
       if (sites[i + k].rank > top_rank) top_rank = sites[i + k].rank;
     const int rank_tiles = top_rank <= 16 ? 1 : (top_rank <= 32 ? 2 : kDownRanks / 16);
+    const int down_ranks = tile ? rank_tiles * 16 : 16;
+    int64_t workgroups = 0;
+    const int outputs = one_outputs(sites + i, p.n, tokens, &workgroups);
     int down = 0, up = 0;
     for (int k = 0; k < p.n; ++k) {
       const seedlm_lora_site& in = sites[i + k];
@@ -506,22 +665,31 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
       o.rows = (int)in.rows;
       o.cols = (int)in.cols;
       o.rank = in.rank;
-      o.chunk_cols = chunk_cols_of(in, p.n, tokens, tile);
+      o.chunk_cols = chunk_cols_of(in, p.n, tokens, kind);
       o.chunks = (o.cols + o.chunk_cols - 1) / o.chunk_cols;
-      o.up_outputs = tile ? 2 * kUpOutputs : kThreads;
+      o.up_outputs = kind == kOne ? outputs : (tile ? up_outputs_of(in, p.n, tokens) : kThreads);
       o.wide = wide_site(in);
       o.first_down = down;
       o.first_up = up;
-      down += o.chunks * (tile ? (o.rank + rank_tiles * 16 - 1) / (rank_tiles * 16) : 1);
+      down += o.chunks * ((o.rank + down_ranks - 1) / down_ranks);
       up += (o.rows + o.up_outputs - 1) / o.up_outputs;
-      h += site_floats(in, o.chunk_cols, tokens);
+      if (kind != kOne) h += site_floats(in, o.chunk_cols, tokens);
     }
-    if (tile) {
+    if (kind == kOne) {
+      if (xdt == SEEDLM_F16) {
+        if (ydt == SEEDLM_F16) run_one<__half, __half>(p, up, s);
+        else run_one<__half, float>(p, up, s);
+      } else {
+        if (ydt == SEEDLM_F16) run_one<float, __half>(p, up, s);
+        else run_one<float, float>(p, up, s);
+      }
+    } else if (tile) {
       const dim3 dg(down, (p.tokens + kDownRows - 1) / kDownRows);
       const dim3 ug(up, (p.tokens + kUpRows - 1) / kUpRows);
-      if (rank_tiles == 1) hipLaunchKernelGGL(lora_down_tile_kernel<1>, dg, dim3(kThreads), 0, s, p);
-      else if (rank_tiles == 2) hipLaunchKernelGGL(lora_down_tile_kernel<2>, dg, dim3(kThreads), 0, s, p);
-      else hipLaunchKernelGGL(lora_down_tile_kernel<4>, dg, dim3(kThreads), 0, s, p);
+      const auto down_kernel = rank_tiles == 1   ? lora_down_tile_kernel<1>
+                               : rank_tiles == 2 ? lora_down_tile_kernel<2>
+                                                 : lora_down_tile_kernel<kDownRanks / 16>;
+      hipLaunchKernelGGL(down_kernel, dg, dim3(kThreads), 0, s, p);
       const size_t lds = (size_t)kUpRows * ((top_rank + 15) / 16 * 16 + 4) * sizeof(uint32_t);
       hipLaunchKernelGGL(lora_up_tile_kernel, ug, dim3(kThreads), lds, s, p);
     } else if (xdt == SEEDLM_F16) {

@@ -116,7 +116,10 @@ int check_attend(const seedlm_cache_attend_args* a) {
       c.head_stride >= kMost / c.kv_heads)
     return SEEDLM_E_UNSUPPORTED;
   const int64_t room = (int64_t)a->max_pages * c.page_size;
-  if ((a->max_len < room ? a->max_len : room) > ((int64_t)1 << 30)) return SEEDLM_E_UNSUPPORTED;
+  // Token numbers, and the sums of 128-token units over the requests, are 32-bit.
+  const int64_t cap = a->max_len < room ? a->max_len : room;
+  if (cap > (int64_t)1 << 30 || (cap / 128 + 1) * a->requests > INT32_MAX)
+    return SEEDLM_E_UNSUPPORTED;
   return SEEDLM_OK;
 }
 
