@@ -54,7 +54,8 @@ extern "C" {
  *   lens_out    int32 [n]; may be lens
  *   ring_state_out int32 [2]; may be ring_state
  *   offsets     int32 [n+1]: where each request's new tokens start among all
- *               new tokens, which lie request after request
+ *               new tokens, which lie request after request (sums stop at
+ *               2^31 - 1)
  *   rows, positions, slots  int32 [T]: request, position and slot of each new
  *               token; past the last one -1, 0, -1
  *   ok          int32 [n]: 1 or 0
@@ -70,7 +71,7 @@ extern "C" {
  * needs several workgroups: then 4 (n + 2) bytes of stream scratch are used).
  * Errors: SEEDLM_E_INVALID (null, range, overlap of lens and lens_out),
  * SEEDLM_E_UNSUPPORTED (max_pages * page_size + tokens or pool * page_size of
- * 2^31 or more), SEEDLM_E_NOMEM, SEEDLM_E_DEVICE.
+ * 2^31 or more, tokens or pool above 2^30), SEEDLM_E_NOMEM, SEEDLM_E_DEVICE.
  */
 typedef struct seedlm_cache_plan_args {
   const int32_t* lens;

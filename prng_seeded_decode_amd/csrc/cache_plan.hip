@@ -27,7 +27,6 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxRequests = SEEDLM_MAX_REQUESTS;
 constexpr int kPerThread = kMaxRequests / kThreads;
-constexpr int kTokensPerThread = 4;
 
 struct PlanArgs {
   seedlm_cache_plan_args a;
@@ -35,44 +34,51 @@ struct PlanArgs {
   int32_t* state_dst;  // ring_state_out, likewise
 };
 
-struct Sums {
-  int64_t fresh, need, back;
-};
+// Sums saturate at 2^32 - 1, past every bound they are compared with (saturating
+// sums of counts are still associative, but cannot be taken apart again).
+__device__ uint32_t add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
-// Inclusive sums over the workgroup's threads in thread order; `total` gets the
-// workgroup's sums.
-__device__ Sums block_scan(Sums v, Sums (&lds)[kWaves], Sums* total) {
+template <int kCtrl, int kRows>
+__device__ uint32_t add_dpp(uint32_t v) {
+  return add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRows, 0xF, false));
+}
+
+// Inclusive sum over the wave's lanes: within rows of 16, then across them.
+__device__ uint32_t wave_scan(uint32_t v) {
+  v = add_dpp<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);  // row_bcast:15
+  return add_dpp<0x143, 0xC>(v);  // row_bcast:31
+}
+
+// Sums of N values over the threads before this one (v), in thread order, and over
+// all of them (total).  lds is free on entry and may be used again after the next
+// barrier.
+template <int N>
+__device__ void block_scan(uint32_t (&v)[N], uint32_t (*lds)[N], uint32_t (&total)[N]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t f = __shfl_up(v.fresh, d), n = __shfl_up(v.need, d), b = __shfl_up(v.back, d);
-    if (lane >= d) {
-      v.fresh += f;
-      v.need += n;
-      v.back += b;
-    }
+  for (int k = 0; k < N; ++k) {
+    const uint32_t upto = wave_scan(v[k]);
+    if (lane == 63) lds[wave][k] = upto;
+    v[k] = __shfl_up(upto, 1);
+    if (lane == 0) v[k] = 0;
+    total[k] = 0;
   }
-  __syncthreads();  // earlier readers of lds are done
-  if (lane == 63) lds[wave] = v;
   __syncthreads();
-  Sums before = {0, 0, 0};
-  *total = {0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const Sums s = lds[w];
-    if (w < wave) {
-      before.fresh += s.fresh;
-      before.need += s.need;
-      before.back += s.back;
+  for (int k = 0; k < N; ++k) {
+    uint32_t before = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint32_t s = lds[w][k];
+      if (w == wave) before = total[k];
+      total[k] = add(total[k], s);
     }
-    total->fresh += s.fresh;
-    total->need += s.need;
-    total->back += s.back;
+    v[k] = add(v[k], before);
   }
-  v.fresh += before.fresh;
-  v.need += before.need;
-  v.back += before.back;
-  return v;
 }
 
 // The first i of [0, n) with ends[i] > x (n if none); ends never falls.
@@ -88,13 +94,15 @@ __device__ int first_above(const int32_t* ends, int n, int32_t x) {
 
 // ceil(len / S) and the queue index i places behind `at` (i < pool), whose sums
 // may pass 2^31 but not 2^32.
-__device__ int pages_of(int len, int S) { return (int)(((uint32_t)len + (uint32_t)S - 1u) / (uint32_t)S); }
+__device__ int pages_of(int len, int S) {
+  return (int)(((uint32_t)len + (uint32_t)S - 1u) / (uint32_t)S);
+}
 __device__ uint32_t ring_at(int at, int i, int pool) {
   const uint32_t x = (uint32_t)at + (uint32_t)i;
   return x >= (uint32_t)pool ? x - (uint32_t)pool : x;
 }
 
-__device__ int32_t saturate(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int32_t)v; }
+__device__ int32_t saturate(uint32_t v) { return v > INT32_MAX ? INT32_MAX : (int32_t)v; }
 
 __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) {
   // Inclusive ends of each request's new tokens, new pages and returned pages
@@ -102,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) 
   __shared__ int32_t s_tok[kMaxRequests], s_need[kMaxRequests], s_back[kMaxRequests];
   __shared__ int32_t s_len[kMaxRequests];
   __shared__ uint8_t s_ok[kMaxRequests];
-  __shared__ Sums s_scan[kWaves];
+  __shared__ uint32_t s_first[kWaves][2], s_second[kWaves][1];
   __shared__ int s_taken;
   const seedlm_cache_plan_args& a = p.a;
   const int n = a.requests, S = a.page_size, tid = threadIdx.x;
@@ -118,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) 
 
   // First sums: tokens and returned pages.
   int len[kPerThread], fresh[kPerThread];
-  Sums mine = {0, 0, 0};
+  uint32_t mine[2] = {0, 0};  // new tokens, returned pages
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per) break;
@@ -128,42 +136,43 @@ __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) 
       len[i] = (int)min<int64_t>(max(a.lens[b], 0), cap);
       fresh[i] = a.fresh[b];
     }
-    mine.fresh += max(fresh[i], 0);
-    if (fresh[i] < 0) mine.back += pages_of(len[i], S);
+    mine[0] = add(mine[0], (uint32_t)max(fresh[i], 0));
+    if (fresh[i] < 0) mine[1] = add(mine[1], (uint32_t)pages_of(len[i], S));
   }
-  Sums total;
-  const Sums upto = block_scan(mine, s_scan, &total);
+  uint32_t total[2];
+  block_scan(mine, s_first, total);
   // Second sum: pages needed by the requests whose tokens fit.
   int need[kPerThread];
-  Sums wanted = {0, 0, 0};
-  int64_t end = upto.fresh - mine.fresh, back = upto.back - mine.back;
+  uint32_t wanted[1] = {0};
+  uint32_t end = mine[0], back = mine[1];
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per) break;
     const int b = tid * per + i;
     const int held = pages_of(len[i], S);
     const int64_t grown = (int64_t)len[i] + max(fresh[i], 0);
-    end += max(fresh[i], 0);
-    const bool fits = fresh[i] >= 0 && grown <= cap && end <= a.tokens;
+    end = add(end, (uint32_t)max(fresh[i], 0));
+    const bool fits = fresh[i] >= 0 && grown <= cap && end <= (uint32_t)a.tokens;
     need[i] = fits ? pages_of((int)grown, S) - held : (fresh[i] < 0 ? 0 : -1);
-    wanted.need += max(need[i], 0);
-    if (fresh[i] < 0) back += held;
+    wanted[0] = add(wanted[0], (uint32_t)max(need[i], 0));
+    if (fresh[i] < 0) back = add(back, (uint32_t)held);
     if (b < n) {
       s_tok[b] = saturate(end);
       s_back[b] = saturate(back);
       s_len[b] = len[i];
     }
   }
-  Sums unused;
-  int64_t cum = block_scan(wanted, s_scan, &unused).need - wanted.need;
+  uint32_t all_wanted[1];
+  block_scan(wanted, s_second, all_wanted);
+  uint32_t cum = wanted[0];
   int taken = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per) break;
     const int b = tid * per + i;
     if (b >= n) break;
-    cum += max(need[i], 0);
-    const bool ok = need[i] == 0 || (need[i] > 0 && cum <= count);
+    cum = add(cum, (uint32_t)max(need[i], 0));
+    const bool ok = need[i] == 0 || (need[i] > 0 && cum <= (uint32_t)count);
     if (ok && need[i] > 0) taken = (int)cum;
     s_need[b] = saturate(cum);
     s_ok[b] = ok;
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) 
   taken = s_taken;
   // Pages that come back find room: pool - count entries are free of any page
   // in the queue (more than that come back only if the inputs were wrong).
-  const int returned = (int)min<int64_t>(total.back, pool - count);
+  const int returned = (int)min(total[1], (uint32_t)(pool - count));
   if (blockIdx.x == 0 && tid == 0) {
     a.offsets[0] = 0;
     p.state_dst[0] = (int)ring_at(head, taken, pool);
@@ -227,14 +236,13 @@ __global__ __launch_bounds__(256) void copy_plan_kernel(const int32_t* __restric
   if (i < 2) state[i] = src[n + i];
 }
 
-// Workgroups of a call: one per kThreads * kTokensPerThread tokens (a decode
-// step takes one; 80,000 tokens take 40).  Below that a second workgroup would
-// repeat the sums for less work than they cost.
+// Workgroups of a call: a token per thread, since a thread's tokens would wait for
+// one another's bisection and page number (80,000 tokens: 7 us a call, 12 with four
+// tokens each), up to two workgroups per compute unit.
 int plan_grid(const seedlm_cache_plan_args& a) {
-  const int64_t per = (int64_t)kThreads * kTokensPerThread;
-  const int64_t items = a.tokens > a.requests ? a.tokens : a.requests;
-  const int64_t g = (items + per - 1) / per;
-  return (int)(g < 1 ? 1 : (g > 256 ? 256 : g));
+  const int g = (a.tokens + kThreads - 1) / kThreads;
+  const int most = 2 * device_cu_count();
+  return g < 1 ? 1 : (g > most ? most : g);
 }
 
 }  // namespace

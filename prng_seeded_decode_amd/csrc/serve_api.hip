@@ -42,8 +42,9 @@ int check_plan(const seedlm_cache_plan_args* a) {
     return SEEDLM_E_INVALID;
   if (a->ring_state_out != a->ring_state && overlap(a->ring_state_out, 2, a->ring_state, 2))
     return SEEDLM_E_INVALID;
+  // Token positions, slots and the kernels' counters are 32-bit.
   if ((int64_t)a->max_pages * a->page_size + a->tokens > INT32_MAX ||
-      (int64_t)a->pool * a->page_size > INT32_MAX)
+      (int64_t)a->pool * a->page_size > INT32_MAX || a->tokens > 1 << 30 || a->pool > 1 << 30)
     return SEEDLM_E_UNSUPPORTED;
   return SEEDLM_OK;
 }

@@ -152,3 +152,21 @@ def test_plan_on_a_strided_table_another_stream_and_a_graph():
         now = (np.array(want["lens_out"]), fresh, np.array(want["table"]), np.array(want["ring"]),
                np.array(want["ring_state_out"]))
     assert (big[:, :2] == -1).all() and (big[:, 10:] == -1).all()
+
+
+def test_plan_of_counts_whose_sums_pass_32_bits():
+    # 600 requests ask for 2^31 - 1 tokens each between ones that ask for a few: those fit no
+    # table, offsets stop at 2^31 - 1, and whoever comes before the first gets its pages
+    big = 2 ** 31 - 1
+    fresh = np.full(600, big)
+    fresh[:5] = [1, 16, 0, -1, 3]
+    fresh[300:310] = 2
+    lens = np.zeros(600, np.int64)
+    lens[3] = 20
+    table = np.full((600, 4), -1)
+    table[3, :2] = [9, 4]
+    ring = np.array([0, 1, 2, 3, 5, 6, 7, 8, -1, -1])
+    got, want = run(lens, fresh, table, ring, (0, 8), 16, 64), R.plan(lens, fresh, table, ring, (0, 8), 16, 64)
+    want["offsets"] = [min(v, big) for v in want["offsets"]]
+    for k in want:
+        assert got[k] == want[k], k

@@ -54,7 +54,8 @@ def attend(V, c=None, **kw):
     ({"lens": P + 2}, "E_INVALID"), ({"lens_out": P + 4}, "E_INVALID"),
     ({"lens_out": P - 8}, "E_INVALID"), ({"ring_state_out": P + 4}, "E_INVALID"),
     ({"max_pages": 2 ** 27, "table_stride": 2 ** 27}, "E_UNSUPPORTED"),
-    ({"pool": 2 ** 27}, "E_UNSUPPORTED"),
+    ({"pool": 2 ** 27}, "E_UNSUPPORTED"), ({"tokens": 2 ** 30 + 1}, "E_UNSUPPORTED"),
+    ({"pool": 2 ** 30 + 1, "page_size": 1}, "E_UNSUPPORTED"),
 ])
 def test_plan_refuses(change, status):
     S, V = _mod()
