@@ -146,7 +146,8 @@ def test_lora_refuses(change, status):
 def test_lora_scratch_is_the_largest_groups():
     S, V = _mod()
     n = ctypes.c_size_t(0)
-    arr = (V._LoraSite * 17)(*[V._LoraSite(P, P, P, P, P, 64, 32, 8)] * 17)
+    # rank 32: no site takes the one-launch form, which needs none
+    arr = (V._LoraSite * 17)(*[V._LoraSite(P, P, P, P, P, 64, 32, 32)] * 17)
 
     def ask(k):
         assert S.lib().seedlm_lora_scratch_bytes(ctypes.cast(arr, ctypes.c_void_p), k, 4, 1, 1,
