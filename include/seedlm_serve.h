@@ -1,8 +1,8 @@
 /*
  * seedlm_serve.h -- what a serving step needs around the packed projections of
  * seedlm.h: page tables and slots of a paged key-value cache, rotary positions
- * with the cache write, attention of one new token per request over the cache,
- * and low-rank adapters of many requests beside a shared projection.
+ * with the cache write, attention of new tokens over the cache, and low-rank
+ * adapters of many requests beside a shared projection.
  *
  * Conventions are those of seedlm.h: status codes, dtype codes, streams passed
  * as void*, device pointers of the current device, asynchronous launches, no
@@ -30,7 +30,7 @@
 extern "C" {
 #endif
 
-/* Most requests of one seedlm_cache_plan or seedlm_cache_attend call. */
+/* Most requests of one seedlm_cache_plan call and queries of a seedlm_cache_attend. */
 #define SEEDLM_MAX_REQUESTS 4096
 /* Largest adapter rank. */
 #define SEEDLM_MAX_RANK 256
@@ -58,6 +58,8 @@ extern "C" {
  *               2^31 - 1)
  *   rows, positions, slots  int32 [T]: request, position and slot of each new
  *               token; past the last one -1, 0, -1
+ *   spans       int32 [T] or NULL: the tokens that each new token attends to,
+ *               position + 1, itself among them; 0 where its slot is -1
  *   ok          int32 [n]: 1 or 0
  * A request's step is granted (ok = 1) if its tokens fit its table row and the
  * T entries, and the queue holds its new pages after those of the requests
@@ -86,6 +88,7 @@ typedef struct seedlm_cache_plan_args {
   int32_t* positions;
   int32_t* slots;
   int32_t* ok;
+  int32_t* spans;
   int64_t table_stride;
   int32_t requests, page_size, max_pages, pool, tokens;
 } seedlm_cache_plan_args;
@@ -141,24 +144,31 @@ typedef struct seedlm_cache_append_args {
 SEEDLM_API int seedlm_cache_append(const seedlm_cache_append_args* args, void* stream);
 
 /*
- * seedlm_cache_attend -- attention of one query token per request over its
- * tokens of the cache: out = sum_t softmax_t(scale * q . k_t) v_t for every
- * head, head h reading cache head h / (heads / kv_heads).
- *   q      [requests][heads][head_dim], row stride q_stride elements
+ * seedlm_cache_attend -- attention of query tokens over their requests' pages of
+ * the cache, one token per request or several: out = sum_t softmax_t(scale *
+ * q . k_t) v_t for every head, head h reading cache head h / (heads / kv_heads).
+ *   q      [queries][heads][head_dim], row stride q_stride elements
  *   out    as q, row stride out_stride; may be q
  *          both of x_dtype (SEEDLM_F32 or SEEDLM_F16)
- *   table  int32 [requests][max_pages], row stride table_stride
- *   lens   int32 [requests]: tokens each request attends to, the new one
- *          among them; taken into [0, min(max_len, max_pages * page_size)]
+ *   table  int32 [table_rows][max_pages], row stride table_stride
+ *   rows   int32 [queries]: each query's row of table, or NULL: its own number
+ *          (then table_rows >= queries).  A row outside [0, table_rows) has no
+ *          tokens
+ *   lens   int32 [queries]: tokens each query attends to, its own among them;
+ *          taken into [0, min(max_len, max_pages * page_size)].  With one token
+ *          per request that is the requests' lengths after seedlm_cache_plan, with
+ *          rows of a plan its spans (several tokens of a request then see one
+ *          another as their positions allow)
  *   max_len  bound on lens that the host knows (the work is split by the
  *          lengths themselves, which only the GPU reads)
  *   scale  finite
- * head_dim 64, 128 or 256; heads a multiple of kv_heads, at most 16384.  A request of no
- * tokens (length 0, or no valid page) gets zeros.  What lies in the cache
- * beyond a request's length, NaN and infinities included, does not reach its
- * output.  Products of fp16 keys are exact; scores, softmax statistics and
- * sums are fp32, and the softmax weights enter the matrix cores as the sum of
- * two fp16 numbers (22 bits), as do fp32 queries.
+ * head_dim 64, 128 or 256; heads a multiple of kv_heads, at most 16384; queries
+ * at most SEEDLM_MAX_REQUESTS.  A query of no tokens (length 0, no row, or no
+ * valid page) gets zeros.  What lies in the cache beyond a query's length, NaN
+ * and infinities included, does not reach its output; an infinity among the
+ * values that it does attend to makes it NaN.  Products of fp16 keys are exact;
+ * scores, softmax statistics and sums are fp32, and the softmax weights enter
+ * the matrix cores as the sum of two fp16 numbers (22 bits), as do fp32 queries.
  * The cache's base addresses are 16-byte aligned and its strides multiples of
  * 8 elements; a pool spans less than 2^35 elements.  fp16 q is 16-byte aligned with
  * a q_stride that is a multiple of 8; fp32 q likewise, of 4.
@@ -172,10 +182,11 @@ typedef struct seedlm_cache_attend_args {
   const void* q;
   void* out;
   const int32_t* table;
+  const int32_t* rows;
   const int32_t* lens;
   seedlm_cache_t cache;
   int64_t q_stride, out_stride, table_stride;
-  int32_t requests, heads, max_pages, max_len, x_dtype;
+  int32_t queries, table_rows, heads, max_pages, max_len, x_dtype;
   float scale;
 } seedlm_cache_attend_args;
 SEEDLM_API int seedlm_cache_attend(const seedlm_cache_attend_args* args, void* stream);

@@ -20,7 +20,7 @@ _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 class _PlanArgs(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("lens", "fresh", "table", "ring", "ring_state", "lens_out",
                                    "ring_state_out", "offsets", "rows", "positions", "slots",
-                                   "ok")] + [
+                                   "ok", "spans")] + [
         ("table_stride", _i64), ("requests", _i32), ("page_size", _i32), ("max_pages", _i32),
         ("pool", _i32), ("tokens", _i32)]
 
@@ -40,9 +40,9 @@ class _AppendArgs(ctypes.Structure):
 
 
 class _AttendArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("q", "out", "table", "lens")] + [
+    _fields_ = [(n, _vp) for n in ("q", "out", "table", "rows", "lens")] + [
         ("cache", _Cache), ("q_stride", _i64), ("out_stride", _i64), ("table_stride", _i64),
-        ("requests", _i32), ("heads", _i32), ("max_pages", _i32), ("max_len", _i32),
+        ("queries", _i32), ("table_rows", _i32), ("heads", _i32), ("max_pages", _i32), ("max_len", _i32),
         ("x_dtype", _i32), ("scale", ctypes.c_float)]
 
 
@@ -71,14 +71,15 @@ def _ints(what, t, n):
     return t.data_ptr()
 
 
-def _table(table, requests):
+def _table(table):
     import torch
 
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != requests:
-        raise ValueError("table must be an int32 tensor [requests][max_pages]")
+    if table.dtype != torch.int32 or table.dim() != 2:
+        raise ValueError("table must be an int32 tensor [rows][max_pages]")
     if table.shape[1] > 1 and table.stride(1) != 1:
         raise ValueError("the rows of table must be contiguous")
-    return table.data_ptr(), table.shape[1], table.stride(0) if requests > 1 else table.shape[1]
+    return (table.data_ptr(), table.shape[1],
+            table.stride(0) if table.shape[0] > 1 else table.shape[1])
 
 
 def _heads(what, t, tokens, heads, dim, dtype):
@@ -116,7 +117,11 @@ class _Call:
 
     def __call__(self, stream=None):
         """Run on `stream` (default: the one given at construction, else torch's
-        current stream)."""
+        current stream), with the tensors' device current."""
+        import torch
+
+        if torch.cuda.current_device() != self._device:
+            raise ValueError("the tensors' device must be the current one")
         sp = _stream_ptr(stream) if stream is not None or self._stream is None else self._stream
         st = self._fn(*self._args, sp)
         if st != OK:
@@ -128,23 +133,26 @@ class CachePlanCall(_Call):
 
     lens, fresh, lens_out, ok: int32 [requests]; table: int32 [requests][max_pages]; ring:
     int32 [pages of the cache]; ring_state, ring_state_out: int32 [2]; offsets: int32
-    [requests + 1]; rows, positions, slots: int32 [tokens].  lens_out may be lens and
-    ring_state_out ring_state."""
+    [requests + 1]; rows, positions, slots and, where wanted, spans: int32 [tokens].  lens_out
+    may be lens and ring_state_out ring_state."""
 
     def __init__(self, lens, fresh, table, ring, ring_state, page_size, lens_out,
-                 ring_state_out, offsets, rows, positions, slots, ok, stream=None):
+                 ring_state_out, offsets, rows, positions, slots, ok, stream=None, spans=None):
         keep = (lens, fresh, table, ring, ring_state, lens_out, ring_state_out, offsets, rows,
-                positions, slots, ok)
+                positions, slots, ok) + (() if spans is None else (spans,))
         device = _on_device(keep)
         n, tokens = lens.numel(), rows.numel()
-        at, max_pages, stride = _table(table, n)
+        if table.shape[0] != n:
+            raise ValueError("table must have a row for each request")
+        at, max_pages, stride = _table(table)
         args = _PlanArgs(
             _ints("lens", lens, n), _ints("fresh", fresh, n), at,
             _ints("ring", ring, ring.numel()), _ints("ring_state", ring_state, 2),
             _ints("lens_out", lens_out, n), _ints("ring_state_out", ring_state_out, 2),
             _ints("offsets", offsets, n + 1), _ints("rows", rows, tokens),
             _ints("positions", positions, tokens), _ints("slots", slots, tokens),
-            _ints("ok", ok, n), stride, n, page_size, max_pages, ring.numel(), tokens)
+            _ints("ok", ok, n), None if spans is None else _ints("spans", spans, tokens), stride, n,
+            page_size, max_pages, ring.numel(), tokens)
         self._set("seedlm_cache_plan", lib().seedlm_cache_plan, (ctypes.byref(args),), keep,
                   device, stream)
 
@@ -190,30 +198,35 @@ class CacheAppendCall(_Call):
 
 
 class CacheAttendCall(_Call):
-    """Attention of one query token per request over its pages (seedlm_cache_attend).
+    """Attention of query tokens over their requests' pages (seedlm_cache_attend).
 
-    q, out: [requests][heads][head_dim], float16 or float32, their rows contiguous; k_cache,
-    v_cache: as for CacheAppendCall; table: int32 [requests][max_pages]; lens: int32
-    [requests], the new token counted.  scale defaults to head_dim ** -0.5, max_len (the
-    host's bound on lens) to what the table can hold.  out may be q."""
+    q, out: [queries][heads][head_dim], float16 or float32, their rows contiguous; k_cache,
+    v_cache: as for CacheAppendCall; table: int32 [table_rows][max_pages]; rows: int32
+    [queries], each query's row of table (default: its own number); lens: int32 [queries],
+    the tokens each query attends to, its own among them (a plan's lens_out, or its spans
+    with its rows).  scale defaults to head_dim ** -0.5, max_len (the host's bound on lens)
+    to what the table can hold.  out may be q."""
 
     def __init__(self, q, k_cache, v_cache, table, lens, out, scale=None, max_len=None,
-                 stream=None):
-        keep = (q, k_cache, v_cache, table, lens, out)
+                 stream=None, rows=None):
+        keep = (q, k_cache, v_cache, table, lens, out) + (() if rows is None else (rows,))
         device = _on_device(keep)
         cache = _cache(k_cache, v_cache)
         if q.dim() != 3:
-            raise ValueError("q must be [requests][heads][head_dim]")
+            raise ValueError("q must be [queries][heads][head_dim]")
         n, heads, dim = q.shape
         if dim != cache.head_dim:
             raise ValueError("q and the caches must have the same head_dim")
-        at, max_pages, stride = _table(table, n)
+        at, max_pages, stride = _table(table)
+        if rows is None and table.shape[0] < n:
+            raise ValueError("without rows, table must have a row for each query")
         code = _dtype_code(q)
         room = max_pages * cache.page_size
         args = _AttendArgs(
-            q.data_ptr(), out.data_ptr(), at, _ints("lens", lens, n), cache,
+            q.data_ptr(), out.data_ptr(), at, None if rows is None else _ints("rows", rows, n),
+            _ints("lens", lens, n), cache,
             _heads("q", q, n, heads, dim, q.dtype), _heads("out", out, n, heads, dim, q.dtype),
-            stride, n, heads, max_pages, room if max_len is None else min(max_len, room), code,
+            stride, n, table.shape[0], heads, max_pages, room if max_len is None else min(max_len, room), code,
             dim ** -0.5 if scale is None else scale)
         self._set("seedlm_cache_attend", lib().seedlm_cache_attend, (ctypes.byref(args),), keep,
                   device, stream)
@@ -282,10 +295,10 @@ class LoraCall(_Call):
 
 
 def seedlm_cache_plan(lens, fresh, table, ring, ring_state, page_size, lens_out, ring_state_out,
-                      offsets, rows, positions, slots, ok, stream=None):
+                      offsets, rows, positions, slots, ok, stream=None, spans=None):
     """One call of CachePlanCall; returns (offsets, rows, positions, slots, ok)."""
     CachePlanCall(lens, fresh, table, ring, ring_state, page_size, lens_out, ring_state_out,
-                  offsets, rows, positions, slots, ok, stream)()
+                  offsets, rows, positions, slots, ok, stream, spans)()
     return offsets, rows, positions, slots, ok
 
 
@@ -298,9 +311,9 @@ def seedlm_cache_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_c
 
 
 def seedlm_cache_attend(q, k_cache, v_cache, table, lens, out, scale=None, max_len=None,
-                        stream=None):
+                        stream=None, rows=None):
     """One call of CacheAttendCall; returns out."""
-    CacheAttendCall(q, k_cache, v_cache, table, lens, out, scale, max_len, stream)()
+    CacheAttendCall(q, k_cache, v_cache, table, lens, out, scale, max_len, stream, rows)()
     return out
 
 

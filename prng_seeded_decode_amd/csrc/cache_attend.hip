@@ -1,5 +1,6 @@
-// Attention of one query token per request over its pages of an fp16 cache
-// (seedlm_cache_attend): out = sum_t softmax_t(scale q . k_t) v_t.
+// Attention of query tokens over their requests' pages of an fp16 cache
+// (seedlm_cache_attend): out = sum_t softmax_t(scale q . k_t) v_t.  A query is
+// called a request here; rows of the table tell which pages it has.
 //
 // Every key and value is read once, with 4 flops per query head of the group
 // that shares it (4 to 8 flops per byte at 8 query heads), so memory bandwidth
@@ -69,7 +70,11 @@ struct AttendArgs {
   float* acc;           // [2 * slots][heads][D]
 };
 
-__device__ int length_of(const AttendArgs& p, int b) { return min(max(p.a.lens[b], 0), p.cap); }
+// A query's tokens; 0 for one without a row of the table.
+__device__ int length_of(const AttendArgs& p, int b) {
+  const int len = min(max(p.a.lens[b], 0), p.cap);
+  return !p.a.rows || (uint32_t)p.a.rows[b] < (uint32_t)p.a.table_rows ? len : 0;
+}
 
 // The first unit of a slot among `units`, and the slot of a unit: the largest i
 // with i * units / slots <= u, that is i * units < (u + 1) * slots.
@@ -84,7 +89,7 @@ __device__ int slot_of(int u, int units, int slots) {
 // taking consecutive requests.
 __device__ void sum_units(const AttendArgs& p, int32_t* ends) {
   __shared__ int s_wave[kWaves];
-  const int n = p.a.requests, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = p.a.queries, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per = (n + kThreads - 1) / kThreads;
   const int b0 = min((int)threadIdx.x * per, n), b1 = min(b0 + per, n);
   int mine = 0;
@@ -123,6 +128,12 @@ __device__ uint32_t pack_rtz(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
 
+template <bool STREAM, typename T>
+__device__ T load(const uint16_t* p) {
+  const T* q = reinterpret_cast<const T*>(p);
+  return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
+
 template <typename T>
 __device__ void store4(T* p, floatx4 v) {
   if constexpr (sizeof(T) == 4) {
@@ -135,13 +146,13 @@ __device__ void store4(T* p, floatx4 v) {
 
 // Waves of attend_kernel per SIMD, and so workgroups per compute unit: what the
 // registers of each form allow.
-__host__ __device__ constexpr int waves_per_simd(int D, bool wide) {
-  return D == 64 ? (wide ? 3 : 4) : (D == 128 ? 2 : 1);
+__host__ __device__ constexpr int waves_per_simd(int D) {
+  return D == 64 ? 3 : (D == 128 ? 2 : 1);
 }
 
-// WIDE: fp32 q and out, else fp16.
-template <int D, bool WIDE>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kernel(const AttendArgs p) {
+// WIDE: fp32 q and out, else fp16.  STREAM: keys and values pass the caches.
+template <int D, bool WIDE, bool STREAM>
+__global__ __launch_bounds__(kThreads, waves_per_simd(D)) void attend_kernel(const AttendArgs p) {
   using T = std::conditional_t<WIDE, float, __half>;
   constexpr int KC = D / 32;              // key operands of a token
   constexpr int VD = D < 128 ? D / 16 : 8;  // consecutive dimensions of a value load
@@ -162,9 +173,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
   int unit = 0, unit_end = 1, run_begin = 0;
   if (p.slots > 0) {
     sum_units(p, s_ends);
-    const int units = s_ends[a.requests - 1];
+    const int units = s_ends[a.queries - 1];
     if (blockIdx.x == 0 && blockIdx.y == 0)
-      for (int b = threadIdx.x; b < a.requests; b += kThreads) p.ends[b] = s_ends[b];
+      for (int b = threadIdx.x; b < a.queries; b += kThreads) p.ends[b] = s_ends[b];
     const int slots = min(p.slots, units);  // none is empty
     if ((int)blockIdx.y >= slots) return;
     run_begin = unit = slot_begin(blockIdx.y, units, slots);
@@ -176,7 +187,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
     bool whole = true;
     const bool starts_run = unit == run_begin;
     if (p.slots > 0) {
-      request = request_of(s_ends, a.requests, unit);
+      request = request_of(s_ends, a.queries, unit);
       const int u0 = request > 0 ? s_ends[request - 1] : 0, u1 = s_ends[request];
       const int upto = min(u1, unit_end);
       begin = (unit - u0) * kUnit;
@@ -231,9 +242,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
       }
     }
 
-    const uint16_t* kbase = static_cast<const uint16_t*>(a.cache.k) + hk * a.cache.head_stride + g * 8;
-    const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + hk * a.cache.head_stride + m * VD;
-    const int32_t* table = a.table + request * a.table_stride;
+    const int64_t head_at = hk * a.cache.head_stride;
+    const uint16_t* kbase = static_cast<const uint16_t*>(a.cache.k) + head_at + g * 8;
+    const uint16_t* vbase = static_cast<const uint16_t*>(a.cache.v) + head_at + m * VD;
+    const int32_t* table = a.table + (a.rows ? a.rows[request] : request) * a.table_stride;
 
     // Tile i of this wave: tokens first + 128 i + (0..31); lane l looks after
     // token l % 32.
@@ -256,7 +268,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
     // Offsets of the tile that was looked up, and its keys requested.
     auto next_keys = [&]() {
       const bool ok = (uint32_t)page < (uint32_t)a.cache.pages;
-      const uint32_t off = ok ? (uint32_t)page * p.page_unit + (uint32_t)nth * p.token_unit : kNoToken;
+      const uint32_t at = (uint32_t)page * p.page_unit + (uint32_t)nth * p.token_unit;
+      const uint32_t off = ok ? at : kNoToken;
       if (lane < kTile) s_off[wave][lane] = off;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -281,14 +294,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int c = 0; c < KC; ++c)
-          kreg[s][c] = *reinterpret_cast<const v4u*>(kbase + (uint64_t)koff[s] * 8 + c * 32);
+          kreg[s][c] = load<STREAM, v4u>(kbase + (uint64_t)koff[s] * 8 + c * 32);
     };
     auto next_values = [&]() {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int u = 0; u < VU; ++u)
-          vreg[u][j] = *reinterpret_cast<const VT*>(vbase + (uint64_t)voff[j] * 8 + u * 128);
+          vreg[u][j] = load<STREAM, VT>(vbase + (uint64_t)voff[j] * 8 + u * 128);
     };
 
     float top = -INFINITY, sum = 0.f;  // running maximum (log2) and this lane's share of the sum
@@ -311,9 +324,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, WIDE)) void attend_kern
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          s[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_half8(kreg[h][c]), qh[c], s[h], 0, 0, 0);
+          const half8 k = as_half8(kreg[h][c]);
+          s[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[c], s[h], 0, 0, 0);
           if constexpr (WIDE)
-            s[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_half8(kreg[h][c]), ql[c], s[h], 0, 0, 0);
+            s[h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[c], s[h], 0, 0, 0);
         }
       if (i + 1 < tiles) {
         next_keys();
@@ -434,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(const AttendArgs 
   __shared__ __align__(16) floatx4 s_part[kGroups][kLanes];
   const seedlm_cache_attend_args& a = p.a;
   const int b = blockIdx.y, head = blockIdx.x;
-  const int units = p.ends[a.requests - 1], slots = min(p.slots, units);
+  const int units = p.ends[a.queries - 1], slots = min(p.slots, units);
   const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
   // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
   // but the first they start the slot's run.
@@ -495,7 +509,7 @@ int qtiles_of(const seedlm_cache_attend_args& a) {
 // and 11.5 at 512; 8 requests of 32 heads and 64 dimensions, lengths up to 2047, 22
 // and 18.
 bool unsplit(const seedlm_cache_attend_args& a) {
-  const int64_t workgroups = (int64_t)a.requests * a.cache.kv_heads * qtiles_of(a);
+  const int64_t workgroups = (int64_t)a.queries * a.cache.kv_heads * qtiles_of(a);
   int steps = 4 * 128 / a.cache.head_dim;
   if (2 * workgroups >= device_cu_count() && steps < 8) steps *= 2;
   return cap_of(a) <= steps * kUnit;
@@ -504,7 +518,7 @@ bool unsplit(const seedlm_cache_attend_args& a) {
 // Runs of units per cache head: what the chip holds at once.
 int slots_of(const seedlm_cache_attend_args& a) {
   if (unsplit(a)) return 0;
-  const int held = device_cu_count() * waves_per_simd(a.cache.head_dim, a.x_dtype == SEEDLM_F32);
+  const int held = device_cu_count() * waves_per_simd(a.cache.head_dim);
   const int across = a.cache.kv_heads * qtiles_of(a);
   return (held + across - 1) / across;
 }
@@ -519,21 +533,31 @@ Scratch scratch_of(const seedlm_cache_attend_args& a) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Scratch r;
   r.ends = 0;
-  r.ml = up((size_t)a.requests * sizeof(int32_t));
+  r.ml = up((size_t)a.queries * sizeof(int32_t));
   r.acc = r.ml + up(n * sizeof(float2));
   r.bytes = n == 0 ? 0 : r.acc + n * a.cache.head_dim * sizeof(float);
   return r;
+}
+
+// Whether keys and values pass the caches: a call that may read more than the 256
+// MB of the memory-side cache finds nothing of it there the next time.  One request
+// of 131071 tokens 101 -> 97 us, 64 of up to 16384 376 -> 369, 16 of 16384 in 256
+// dimensions 347 -> 323; 64 dimensions gain nothing (442 and 456).  A cache that fits
+// would lose: 16 requests of 2048, read again and again, 29 -> 33 us.
+bool streams(const seedlm_cache_attend_args& a) {
+  const int64_t most = (int64_t)a.queries * cap_of(a) * a.cache.kv_heads * a.cache.head_dim * 4;
+  return a.cache.head_dim > 64 && most > (int64_t)256 << 20;
 }
 
 template <int D, bool WIDE>
 int run(const AttendArgs& p, hipStream_t s) {
   const seedlm_cache_attend_args& a = p.a;
   const bool split = p.slots > 0;
-  hipLaunchKernelGGL((attend_kernel<D, WIDE>),
-                     dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.requests),
-                     dim3(kThreads), split ? a.requests * sizeof(int32_t) : 0, s, p);
+  const auto kernel = streams(a) ? attend_kernel<D, WIDE, (D > 64)> : attend_kernel<D, WIDE, false>;
+  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries),
+                     dim3(kThreads), split ? a.queries * sizeof(int32_t) : 0, s, p);
   if (split)
-    hipLaunchKernelGGL((attend_join_kernel<D, WIDE>), dim3(a.heads, a.requests), dim3(kThreads), 0,
+    hipLaunchKernelGGL((attend_join_kernel<D, WIDE>), dim3(a.heads, a.queries), dim3(kThreads), 0,
                        s, p);
   return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
 }

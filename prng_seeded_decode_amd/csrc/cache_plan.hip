@@ -225,6 +225,7 @@ __global__ __launch_bounds__(kThreads) void cache_plan_kernel(const PlanArgs p) 
     a.rows[t] = row;
     a.positions[t] = pos;
     a.slots[t] = slot;
+    if (a.spans) a.spans[t] = slot >= 0 ? pos + 1 : 0;
   }
 }
 

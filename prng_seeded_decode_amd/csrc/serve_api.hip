@@ -36,7 +36,7 @@ int check_plan(const seedlm_cache_plan_args* a) {
                         (const void*)a->ring, (const void*)a->ring_state,
                         (const void*)a->lens_out, (const void*)a->ring_state_out,
                         (const void*)a->offsets, (const void*)a->ok, (const void*)a->rows,
-                        (const void*)a->positions, (const void*)a->slots})
+                        (const void*)a->positions, (const void*)a->slots, (const void*)a->spans})
     if (!aligned(p, 4)) return SEEDLM_E_INVALID;
   if (a->lens_out != a->lens && overlap(a->lens_out, a->requests, a->lens, a->requests))
     return SEEDLM_E_INVALID;
@@ -93,14 +93,15 @@ int check_attend(const seedlm_cache_attend_args* a) {
   const int st = check_cache(c);
   if (st != SEEDLM_OK) return st;
   if (!a->q || !a->out || !a->table || !a->lens) return SEEDLM_E_INVALID;
-  if (a->requests < 1 || a->requests > SEEDLM_MAX_REQUESTS || a->heads < 1 || a->max_pages < 1 ||
-      a->max_len < 0 || a->table_stride < a->max_pages || a->heads % c.kv_heads != 0)
+  if (a->queries < 1 || a->queries > SEEDLM_MAX_REQUESTS || a->heads < 1 || a->max_pages < 1 ||
+      a->max_len < 0 || a->table_stride < a->max_pages || a->heads % c.kv_heads != 0 ||
+      a->table_rows < 1 || (!a->rows && a->table_rows < a->queries))
     return SEEDLM_E_INVALID;
   if (!(a->scale - a->scale == 0.f)) return SEEDLM_E_INVALID;  // NaN or infinite
   const int64_t row = (int64_t)a->heads * c.head_dim;
   if (a->q_stride < row || a->out_stride < row) return SEEDLM_E_INVALID;
   if (a->out == a->q && a->out_stride != a->q_stride) return SEEDLM_E_INVALID;
-  if (!aligned(a->table, 4) || !aligned(a->lens, 4) ||
+  if (!aligned(a->table, 4) || !aligned(a->lens, 4) || !aligned(a->rows, 4) ||
       !aligned(a->out, (uintptr_t)dtype_bytes(a->x_dtype)))
     return SEEDLM_E_INVALID;
   if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return SEEDLM_E_UNSUPPORTED;
@@ -119,7 +120,7 @@ int check_attend(const seedlm_cache_attend_args* a) {
   const int64_t room = (int64_t)a->max_pages * c.page_size;
   // Token numbers, and the sums of 128-token units over the requests, are 32-bit.
   const int64_t cap = a->max_len < room ? a->max_len : room;
-  if (cap > (int64_t)1 << 30 || (cap / 128 + 1) * a->requests > INT32_MAX)
+  if (cap > (int64_t)1 << 30 || (cap / 128 + 1) * a->queries > INT32_MAX)
     return SEEDLM_E_UNSUPPORTED;
   return SEEDLM_OK;
 }

@@ -252,3 +252,28 @@ def test_attend_reaches_past_32_bit_offsets():
     check(x, run(y))
     del pools, y
     torch.cuda.empty_cache()
+
+
+def test_attend_of_several_queries_per_request():
+    # queries in any order of rows, several of one request at different lengths, rows outside
+    # the table: each equals the same query attending alone
+    import torch
+
+    import prng_seeded_decode_amd as S
+
+    x = make([14], [300, 70, 1000], 8, 2, 128, 16, True)
+    rows = [2, 0, 0, -1, 1, 2, 3, 0, 2 ** 31 - 1, 1]
+    lens = [1000, 300, 17, 50, 70, 513, 20, 0, 1, 1]
+    q = torch.randn((len(rows), 8, 128), device="cuda").half()
+    out = torch.full_like(q, 3.0)
+    S.seedlm_cache_attend(q, x["k_cache"], x["v_cache"], x["dtable"],
+                          torch.tensor(lens, dtype=torch.int32, device="cuda"), out,
+                          rows=torch.tensor(rows, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    for i, (row, n) in enumerate(zip(rows, lens)):
+        if not 0 <= row < 3:
+            n, row = 0, 0
+        ref, tol = R.attend(q[i].double().cpu().numpy(), x["keys"][row][:n], x["values"][row][:n],
+                            np.float64(np.float32(128 ** -0.5)), True)
+        assert np.all(np.abs(got[i] - ref) <= tol), i

@@ -49,10 +49,13 @@ def run(lens, fresh, table, ring, state, size, tokens, in_place=False, stream=No
            zip(NAMES, (n, 2, n + 1, tokens, tokens, tokens, n))}
     if in_place:
         out["lens_out"], out["ring_state_out"] = d["lens"], d["state"]
+    spans = torch.full((tokens,), -99, dtype=torch.int32, device="cuda")
     S.seedlm_cache_plan(d["lens"], d["fresh"], d["table"], d["ring"], d["state"], size,
-                        *(out[k] for k in NAMES), stream=stream)
+                        *(out[k] for k in NAMES), stream=stream, spans=spans)
     torch.cuda.synchronize()
     got = {k: v.cpu().tolist() for k, v in out.items()}
+    assert spans.cpu().tolist() == [p + 1 if s >= 0 else 0
+                                    for p, s in zip(got["positions"], got["slots"])]
     got["table"], got["ring"] = d["table"].cpu().tolist(), d["ring"].cpu().tolist()
     return got
 

@@ -92,6 +92,10 @@ def test_lora_of_few_rows(tokens, rank, sites, kind, x16, y16):
     (129, 64, [(72, 1096)]), (200, 16, [(1024, 1024), (256, 1024), (256, 1024)]),
     (77, 24, [(520, 264)]), (130, 128, [(136, 264)]), (50, 256, [(200, 136)]),
     (40, 5, [(33, 47)]), (65, 20, [(130, 100)]), (35, 16, [(8, 8)]), (257, 48, [(328, 2056)]),
+    # enough products for the matrix cores (64 MB of A and B, counted once per row)
+    (513, 16, [(2056, 2064)]), (129, 256, [(520, 520)]), (300, 64, [(904, 1000)]),
+    (700, 24, [(1032, 968)]), (1030, 8, [(2056, 2056), (264, 2056)]), (200, 128, [(680, 680)]),
+    (2100, 16, [(1000, 1000)]), (64, 240, [(1608, 600)]), (350, 32, [(8, 3000)]),
 ])
 def test_lora_of_many_rows(tokens, rank, sites, kind):
     c = make([tokens, rank, 1], sites, rank, tokens, 5, ids_of([tokens], tokens, 5, kind))
@@ -114,9 +118,13 @@ def test_lora_of_more_sites_than_one_launch_takes():
         check(c, run(c))
 
 
-@pytest.mark.parametrize("tokens", [6, 96])
-def test_lora_keeps_other_adapters_nan_and_infinities_away(tokens):
-    c = make([24], [(264, 512)], 16, tokens, 4, np.arange(tokens) % 4)
+# one launch, the row kernels, the matrix cores
+FORMS = [(6, 16, (264, 512)), (96, 24, (264, 512)), (170, 64, (1032, 2056))]
+
+
+@pytest.mark.parametrize("tokens,rank,site", FORMS)
+def test_lora_keeps_other_adapters_nan_and_infinities_away(tokens, rank, site):
+    c = make([24], [site], rank, tokens, 4, np.arange(tokens) % 4)
     clean = run(c)[0]
     x, A, B, base = c["dev"][0]
     A[1, 3, 100], B[2, 17, 5], x[3, 9] = float("nan"), float("inf"), float("nan")
@@ -130,13 +138,12 @@ def test_lora_keeps_other_adapters_nan_and_infinities_away(tokens):
     assert np.array_equal(got[rest], clean[rest]) and np.isnan(got[3]).all()
 
 
-@pytest.mark.parametrize("tokens", [4, 48])
-def test_lora_of_large_and_small_products(tokens):
+@pytest.mark.parametrize("y16", [True, False])
+@pytest.mark.parametrize("tokens,rank,site", FORMS)
+def test_lora_of_large_and_small_products(tokens, rank, site, y16):
     # A x beyond fp16's range, and far below its normal numbers
     for power in (9, -20):
-        c = make([25], [(136, 512)], 16, tokens, 3, np.arange(tokens) % 3, True, False)
-        if tokens > 16:
-            c = make([25], [(136, 512)], 16, tokens, 3, np.arange(tokens) % 3)
+        c = make([25], [site], rank, tokens, 3, np.arange(tokens) % 3, True, y16)
         s = c["host"][0]
         s["x"] = (s["x"].astype(np.float64) * 2.0 ** power).astype(np.float16)
         s["A"] = (s["A"].astype(np.float64) * (2.0 ** 9 if power > 0 else 1)).astype(np.float16)
@@ -149,13 +156,13 @@ def test_lora_of_large_and_small_products(tokens):
         check(c, run(c))
 
 
-@pytest.mark.parametrize("tokens", [5, 70])
-def test_lora_on_another_stream_and_in_a_graph(tokens):
+@pytest.mark.parametrize("tokens,rank,site", FORMS)
+def test_lora_on_another_stream_and_in_a_graph(tokens, rank, site):
     import torch
 
     import prng_seeded_decode_amd as S
 
-    c = make([26], [(512, 776), (128, 776)], 16, tokens, 4, ids_of([3], tokens, 4, "mixed"))
+    c = make([26], [site, (128, site[1])], rank, tokens, 4, ids_of([3], tokens, 4, "mixed"))
     plain = run(c)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())

@@ -16,7 +16,7 @@ P = 4096  # an aligned address that is never used
 
 
 def plan(V, **kw):
-    a = V._PlanArgs(*([P] * 12), 8, 4, 16, 8, 100, 32)
+    a = V._PlanArgs(*([P] * 12), None, 8, 4, 16, 8, 100, 32)
     a.lens_out, a.ring_state_out = 2 * P, 2 * P
     for k, v in kw.items():
         setattr(a, k, v)
@@ -38,7 +38,7 @@ def append(V, c=None, **kw):
 
 
 def attend(V, c=None, **kw):
-    a = V._AttendArgs(*([P] * 4), c or cache(V), 256, 256, 8, 3, 4, 8, 100, 1, 0.1)
+    a = V._AttendArgs(P, P, P, None, P, c or cache(V), 256, 256, 8, 3, 3, 4, 8, 100, 1, 0.1)
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -51,7 +51,7 @@ def attend(V, c=None, **kw):
     ({"requests": 0}, "E_INVALID"), ({"requests": 4097}, "E_INVALID"),
     ({"page_size": 0}, "E_INVALID"), ({"max_pages": 0}, "E_INVALID"), ({"pool": 0}, "E_INVALID"),
     ({"tokens": -1}, "E_INVALID"), ({"table_stride": 7}, "E_INVALID"),
-    ({"lens": P + 2}, "E_INVALID"), ({"lens_out": P + 4}, "E_INVALID"),
+    ({"spans": P + 1}, "E_INVALID"), ({"lens": P + 2}, "E_INVALID"), ({"lens_out": P + 4}, "E_INVALID"),
     ({"lens_out": P - 8}, "E_INVALID"), ({"ring_state_out": P + 4}, "E_INVALID"),
     ({"max_pages": 2 ** 27, "table_stride": 2 ** 27}, "E_UNSUPPORTED"),
     ({"pool": 2 ** 27}, "E_UNSUPPORTED"), ({"tokens": 2 ** 30 + 1}, "E_UNSUPPORTED"),
@@ -93,8 +93,9 @@ def test_append_refuses(c, change, status):
     ({"page_stride": 2 ** 34}, {}, "E_UNSUPPORTED"), ({"token_stride": 2 ** 33}, {}, "E_UNSUPPORTED"),
     ({"head_stride": 2 ** 35}, {}, "E_UNSUPPORTED"),
     *[({}, {k: None}, "E_INVALID") for k in ("q", "out", "table", "lens")],
-    ({}, {"x_dtype": -1}, "E_UNSUPPORTED"), ({}, {"requests": 0}, "E_INVALID"),
-    ({}, {"requests": 4097}, "E_INVALID"), ({}, {"heads": 3}, "E_INVALID"),
+    ({}, {"x_dtype": -1}, "E_UNSUPPORTED"), ({}, {"queries": 0}, "E_INVALID"),
+    ({}, {"queries": 4097}, "E_INVALID"), ({}, {"table_rows": 2}, "E_INVALID"),
+    ({}, {"table_rows": 0, "rows": P}, "E_INVALID"), ({}, {"rows": P + 2}, "E_INVALID"), ({}, {"heads": 3}, "E_INVALID"),
     ({}, {"max_pages": 0}, "E_INVALID"), ({}, {"max_len": -1}, "E_INVALID"),
     ({}, {"table_stride": 7}, "E_INVALID"), ({}, {"q_stride": 255}, "E_INVALID"),
     ({}, {"out_stride": 264}, "E_INVALID"), ({}, {"q": P + 8}, "E_UNSUPPORTED"),
