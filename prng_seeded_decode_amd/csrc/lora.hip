@@ -17,7 +17,7 @@
 //   down  32 rows and up to 64 ranks per workgroup, x and A staged through LDS
 //   up    16 rows and 128 outputs per wave and step; the sums turn over in LDS.  h
 //         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
-//         largest |h|), the 16 high and 16 low parts of 16 ranks filling the 32
+//         largest |h|); up to rank 16 the 16 high and 16 low parts fill the 32
 //         products of one MFMA against the same 16 elements of B twice.
 // A tile whose rows have several adapters takes them one after another and keeps
 // each result for its own rows only, so no adapter's values reach another's rows.
@@ -383,11 +383,20 @@ __global__ __launch_bounds__(kThreads) void lora_down_tile_kernel(const LoraArgs
   }
 }
 
-// y of kUpRows rows and s.up_outputs outputs; wave w has rows 16 w + (0..15).
+// The chosen 16-bit halves of 8 words, packed.
+__device__ v4u parts(v4u p0, v4u p1, uint32_t select) {
+  const auto pick = [&](uint32_t hi, uint32_t lo) { return __builtin_amdgcn_perm(hi, lo, select); };
+  return v4u{pick(p0[1], p0[0]), pick(p0[3], p0[2]), pick(p1[1], p1[0]), pick(p1[3], p1[2])};
+}
+
+// y of kUpRows rows and s.up_outputs outputs; wave w has rows 16 w + (0..15).  BLOCK:
+// ranks of a pass, 16 (for at most 16: high and low parts in one MFMA, B twice) or 32
+// (an MFMA each, on one load of B).
+template <int BLOCK>
 __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p) {
-  // h of the rows, each value as hi | lo << 16, ranks padded with zeros to
-  // sixteens; the factor scales[a] * 2^e of each row; and a wave's sums of a step,
-  // turned over so that base and y are read and written in runs of 256 bytes
+  // h of the rows, each value as hi | lo << 16, ranks padded with zeros to BLOCKs;
+  // the factor scales[a] * 2^e of each row; and a wave's sums of a step, turned over
+  // so that base and y are read and written in runs of 256 bytes
   extern __shared__ __align__(16) uint32_t s_pair[];
   __shared__ float s_factor[kUpRows];
   __shared__ __align__(16) float s_sum[kWaves][16][kUpStep + 4];
@@ -395,21 +404,53 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m = lane & 15, g = lane >> 4;
   const int t0 = blockIdx.y * kUpRows;
-  const int ranks = (s.rank + 15) / 16 * 16, stride = ranks + 4;
+  const int ranks = (s.rank + BLOCK - 1) / BLOCK * BLOCK, stride = ranks + 4;
   const int id = adapter_of_lane(p, t0, kUpRows, lane);
+  const int r0 = wave * 16;  // the wave's rows, but in the next block
+  const bool copies = s.y != s.base;
+  const uint32_t has = (uint32_t)(__ballot(id >= 0) >> r0) & 0xFFFF;
+  // This lane's 8 ranks of a block, and which parts: all high ones, or with BLOCK 16
+  // the low ones for the upper half of the lanes.
+  const int at = BLOCK == 16 ? (g & 1) * 8 : g * 8;
+  const uint32_t high = 0x05040100u, low = 0x07060302u;
+  const uint32_t select = BLOCK == 16 && g >= 2 ? low : high;
+  const int o_begin = (blockIdx.x - s.first_up) * s.up_outputs;
+  const int o_end = min(s.rows, o_begin + s.up_outputs);
+  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows 4 i + l/16.
+  const __half* base = static_cast<const __half*>(s.base) + (int64_t)(t0 + r0) * s.rows + m * 8;
+  __half* y = static_cast<__half*>(s.y) + (int64_t)(t0 + r0) * s.rows + m * 8;
+  v4u bases[4];
+  auto request = [&](int o0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens)
+        bases[i] = __builtin_nontemporal_load(
+            reinterpret_cast<const v4u*>(base + (int64_t)(4 * i + g) * s.rows + o0));
+  };
+  const bool done = t0 + r0 >= p.tokens || (has == 0 && !copies);
+  if (!done) request(o_begin);
   {
     // four threads a row, four ranks at a time
+    constexpr int kAtOnce = 8;
     const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
     const int a = __shfl(id, t);
     float top = 0.f;
     if (a >= 0) {
+#pragma unroll 2
       for (int j = part * 4; j < ranks; j += 16) {
         floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-        if (j < s.rank)
-#pragma unroll 4
-          for (int c = 0; c < s.chunks; ++c)
-            sum += *reinterpret_cast<const floatx4*>(
-                s.h + ((int64_t)c * p.tokens + t0 + t) * s.rank + j);
+        for (int c0 = 0; j < s.rank && c0 < s.chunks; c0 += kAtOnce) {
+          floatx4 v[kAtOnce];  // requested together
+#pragma unroll
+          for (int c = 0; c < kAtOnce; ++c) {
+            v[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+            if (c0 + c < s.chunks)
+              v[c] = *reinterpret_cast<const floatx4*>(
+                  s.h + ((int64_t)(c0 + c) * p.tokens + t0 + t) * s.rank + j);
+          }
+#pragma unroll
+          for (int c = 0; c < kAtOnce; ++c) sum += v[c];
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(sum[i]));
         *reinterpret_cast<floatx4*>(&s_pair[t * stride + j]) = sum;
@@ -437,26 +478,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
     }
   }
   __syncthreads();
-  const int r0 = wave * 16;  // the wave's rows from here on
-  if (t0 + r0 >= p.tokens) return;
-  const bool copies = s.y != s.base;
-  const uint32_t has = (uint32_t)(__ballot(id >= 0) >> r0) & 0xFFFF;
-  if (has == 0 && !copies) return;
-  const uint32_t select = g < 2 ? 0x05040100u : 0x07060302u;  // high or low parts
-  const int o_begin = (blockIdx.x - s.first_up) * s.up_outputs;
-  const int o_end = min(s.rows, o_begin + s.up_outputs);
-  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows 4 i + l/16.
-  const __half* base = static_cast<const __half*>(s.base) + (int64_t)(t0 + r0) * s.rows + m * 8;
-  __half* y = static_cast<__half*>(s.y) + (int64_t)(t0 + r0) * s.rows + m * 8;
-  v4u bases[4];
-  auto request = [&](int o0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens)
-        bases[i] = __builtin_nontemporal_load(
-            reinterpret_cast<const v4u*>(base + (int64_t)(4 * i + g) * s.rows + o0));
-  };
-  request(o_begin);
+  if (done) return;
   for (int o0 = o_begin; o0 < o_end; o0 += kUpStep) {
     uint32_t todo = has;
     while (todo) {
@@ -466,25 +488,27 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
       floatx4 acc[kUpStep / 16];
 #pragma unroll
       for (int u = 0; u < kUpStep / 16; ++u) acc[u] = floatx4{0.f, 0.f, 0.f, 0.f};
-      const __half* B = s.B + (int64_t)a * s.rows * s.rank + (g & 1) * 8;
-      for (int j = 0; j < ranks; j += 16) {
+      const __half* B = s.B + (int64_t)a * s.rows * s.rank + at;
+      for (int j = 0; j < ranks; j += BLOCK) {
         v4u bv[kUpStep / 16];
 #pragma unroll
         for (int u = 0; u < kUpStep / 16; ++u) {
           const int o = min(o0 + 16 * u + m, s.rows - 1);
           bv[u] = v4u{0, 0, 0, 0};
-          if (j + (g & 1) * 8 < s.rank)
+          if (j + at < s.rank)
             bv[u] = *reinterpret_cast<const v4u*>(B + (int64_t)o * s.rank + j);
         }
-        const uint32_t* pair = &s_pair[(r0 + m) * stride + j + (g & 1) * 8];
+        const uint32_t* pair = &s_pair[(r0 + m) * stride + j + at];
         const v4u p0 = *reinterpret_cast<const v4u*>(pair);
         const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
-        const v4u hv = {__builtin_amdgcn_perm(p0[1], p0[0], select),
-                        __builtin_amdgcn_perm(p0[3], p0[2], select),
-                        __builtin_amdgcn_perm(p1[1], p1[0], select),
-                        __builtin_amdgcn_perm(p1[3], p1[2], select)};
+        const v4u hv = parts(p0, p1, select);
 #pragma unroll
         for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], hv, acc[u]);
+        if constexpr (BLOCK == 32) {
+          const v4u lv = parts(p0, p1, low);
+#pragma unroll
+          for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], lv, acc[u]);
+        }
       }
       if ((own >> m) & 1) {
         const float f = s_factor[r0 + m];
@@ -576,13 +600,15 @@ Kind kind_of(const seedlm_lora_site* s, int n, int64_t tokens, int xdt, int ydt)
 
 // Column chunks of a site of an n-site group: kChunk columns each for the row
 // kernels; for the tiles as few as give four workgroups per compute unit, of at
-// least 512 columns.
+// least 512 columns, and not so many that an up workgroup reads more than 64 KiB of
+// their sums (128 where few rows leave few such workgroups).
 int chunk_cols_of(const seedlm_lora_site& s, int n, int64_t tokens, Kind kind) {
   if (kind != kTiles) return kChunk;
   const int64_t across = (tokens + kDownRows - 1) / kDownRows * n;
   int64_t chunks = (4 * device_cu_count() + across - 1) / across;
-  const int64_t most = (s.cols + 511) / 512;
-  if (chunks > most) chunks = most;
+  const int64_t sums = tokens <= 2 * kUpRows ? 512 : 256;
+  for (int64_t most : {(s.cols + 511) / 512, sums / s.rank})
+    if (chunks > most) chunks = most > 0 ? most : 1;
   const int64_t cols = (s.cols + chunks - 1) / chunks;
   return (int)((cols + kDownStep - 1) / kDownStep * kDownStep);
 }
@@ -592,13 +618,17 @@ size_t site_floats(const seedlm_lora_site& s, int chunk_cols, int64_t tokens) {
   return (size_t)((chunks * tokens * s.rank + 63) / 64 * 64);
 }
 
-// Outputs of an up workgroup: as many steps as leave four workgroups per compute
-// unit, at most 4 (every workgroup forms the rows' h again).
-int up_outputs_of(const seedlm_lora_site& s, int n, int64_t tokens) {
-  const int64_t steps = (s.rows + kUpStep - 1) / kUpStep;
-  const int64_t all = (tokens + kUpRows - 1) / kUpRows * steps * n;
-  const int64_t each = all / (4 * device_cu_count());
-  return (int)(each < 1 ? 1 : (each > 4 ? 4 : each)) * kUpStep;
+// Outputs of an up workgroup, which forms the rows' h first: so many steps that the
+// workgroups run in one round of three per compute unit, at most 4; more, while that
+// leaves one per compute unit, where the chunks' sums are more than a step's base and
+// y (32 KiB).
+int up_outputs_of(const seedlm_lora_site& s, int n, int64_t tokens, int chunks) {
+  const int64_t all = (tokens + kUpRows - 1) / kUpRows * ((s.rows + kUpStep - 1) / kUpStep) * n;
+  const int64_t cus = device_cu_count(), round = (all + 3 * cus - 1) / (3 * cus);
+  int64_t each = round > 4 ? 4 : round;
+  const int64_t sums = ((int64_t)s.rank * chunks + 127) / 128, most = all / cus;
+  if (each < sums) each = sums < most ? sums : most;
+  return (int)(each < 1 ? 1 : each) * kUpStep;
 }
 
 int group_size(int n, int i) { return n - i < kLoraGroup ? n - i : kLoraGroup; }
@@ -667,7 +697,9 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
       o.rank = in.rank;
       o.chunk_cols = chunk_cols_of(in, p.n, tokens, kind);
       o.chunks = (o.cols + o.chunk_cols - 1) / o.chunk_cols;
-      o.up_outputs = kind == kOne ? outputs : (tile ? up_outputs_of(in, p.n, tokens) : kThreads);
+      o.up_outputs = kind == kOne ? outputs
+                     : tile       ? up_outputs_of(in, p.n, tokens, o.chunks)
+                                  : kThreads;
       o.wide = wide_site(in);
       o.first_down = down;
       o.first_up = up;
@@ -690,8 +722,10 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
                                : rank_tiles == 2 ? lora_down_tile_kernel<2>
                                                  : lora_down_tile_kernel<kDownRanks / 16>;
       hipLaunchKernelGGL(down_kernel, dg, dim3(kThreads), 0, s, p);
-      const size_t lds = (size_t)kUpRows * ((top_rank + 15) / 16 * 16 + 4) * sizeof(uint32_t);
-      hipLaunchKernelGGL(lora_up_tile_kernel, ug, dim3(kThreads), lds, s, p);
+      const int block = top_rank <= 16 ? 16 : 32;
+      const size_t lds = (size_t)kUpRows * ((top_rank + block - 1) / block * block + 4) * 4;
+      const auto up_kernel = block == 16 ? lora_up_tile_kernel<16> : lora_up_tile_kernel<32>;
+      hipLaunchKernelGGL(up_kernel, ug, dim3(kThreads), lds, s, p);
     } else if (xdt == SEEDLM_F16) {
       if (ydt == SEEDLM_F16) run_rows<__half, __half>(p, down, up, s);
       else run_rows<__half, float>(p, down, up, s);
