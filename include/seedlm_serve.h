@@ -237,7 +237,7 @@ SEEDLM_API int seedlm_lora_many(const seedlm_lora_site* sites, int n, const int3
 /* seedlm_lora_scratch_bytes -- stream scratch that seedlm_lora_many uses for
  * these sites (only their sizes and alignment count).  Errors as there. */
 SEEDLM_API int seedlm_lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens,
-                                         int x_dtype, int y_dtype, size_t* bytes);
+                                         int adapters, int x_dtype, int y_dtype, size_t* bytes);
 
 #ifdef __cplusplus
 }

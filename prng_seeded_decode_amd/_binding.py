@@ -130,7 +130,7 @@ def lib() -> ctypes.CDLL:
     L.seedlm_cache_attend.argtypes = [vp, vp]
     L.seedlm_cache_attend_scratch_bytes.argtypes = [vp, ctypes.POINTER(sz)]
     L.seedlm_lora_many.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, vp]
-    L.seedlm_lora_scratch_bytes.argtypes = [vp, i32, i64, i32, i32, ctypes.POINTER(sz)]
+    L.seedlm_lora_scratch_bytes.argtypes = [vp, i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
     for name in EXPORTED:
         if name != "seedlm_status_string":
             getattr(L, name).restype = i32

@@ -287,8 +287,9 @@ class LoraCall(_Call):
     def scratch_bytes(self) -> int:
         """Stream scratch that the call uses."""
         out = ctypes.c_size_t(0)
-        st = lib().seedlm_lora_scratch_bytes(self._args[0], self._args[1], self._args[4],
-                                             self._args[6], self._args[7], ctypes.byref(out))
+        sites, n, _, _, tokens, adapters, xdt, ydt = self._args
+        st = lib().seedlm_lora_scratch_bytes(sites, n, tokens, adapters, xdt, ydt,
+                                             ctypes.byref(out))
         if st != OK:
             raise SeedLMError(st, "seedlm_lora_scratch_bytes")
         return out.value

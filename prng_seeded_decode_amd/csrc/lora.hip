@@ -14,13 +14,13 @@
 //
 // Many rows (fp16): v_mfma_f32_16x16x32_f16, with A (then B) as the first operand
 // and 16 rows as the second, so that a lane's results belong to one row:
-//   down  32 rows and up to 64 ranks per workgroup, x and A staged through LDS
+//   sort  rows gathered by adapter into tiles of 32, so that a tile has one adapter
+//         however the rows lie
+//   down  a tile and up to 64 ranks per workgroup, x and A staged through LDS
 //   up    16 rows and 128 outputs per wave and step; the sums turn over in LDS.  h
 //         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
 //         largest |h|); up to rank 16 the 16 high and 16 low parts fill the 32
 //         products of one MFMA against the same 16 elements of B twice.
-// A tile whose rows have several adapters takes them one after another and keeps
-// each result for its own rows only, so no adapter's values reach another's rows.
 // The bytes of x, base and y bound these.
 #include <hip/hip_fp16.h>
 
@@ -32,8 +32,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunk = 8 * kThreads;  // columns of a workgroup of the row kernels
-constexpr int kDownRows = 32;    // rows, and ranks at most, of a down tile
-constexpr int kDownRanks = 64;
+constexpr int kTileRows = 32;    // rows of a tile, of one adapter
+constexpr int kDownRanks = 64;   // ranks at most of a down workgroup
 constexpr int kDownStep = 256;   // columns staged at once
 constexpr int kUpRows = 16 * kWaves;  // rows of an up workgroup, 16 per wave
 constexpr int kUpStep = 128;          // outputs of a wave's step
@@ -62,6 +62,10 @@ struct LoraArgs {
   Site s[kLoraGroup];
   const int32_t* adapter;
   const float* scales;
+  int32_t* tile_count;  // tiles of the many-row form, their adapters and rows
+  int32_t* tiles;
+  int32_t* order;
+  int32_t* place;
   int n, tokens, adapters;
 };
 
@@ -283,14 +287,85 @@ __device__ floatx4 mfma(v4u a, v4u b, floatx4 c) {
                                                 __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
 
-// The adapter of row t0 + lane (lane < n), -1 for none.
-__device__ int adapter_of_lane(const LoraArgs& p, int t0, int n, int lane) {
-  const int t = t0 + lane;
-  const int a = lane < n && t < p.tokens ? p.adapter[t] : -1;
-  return a < p.adapters ? a : -1;
+// Gathers the rows into tiles of kTileRows rows of one adapter (and of rows without
+// one, whose adapter is -1): tile i has adapter tiles[i] and rows order[kTileRows * i
+// + ..], -1 past its last one.  A counting sort by one workgroup, LDS counters being
+// advanced once per wave and adapter; which place a row gets in its adapter's tiles
+// depends on the order of these, its results do not.
+constexpr int kSortThreads = 1024;
+constexpr int kSortAtOnce = 4;  // rows of a thread requested together
+constexpr int kSortAdapters = 8191;
+
+__global__ __launch_bounds__(kSortThreads) void lora_sort_kernel(const LoraArgs p) {
+  extern __shared__ int s_count[];  // [buckets] rows, then [buckets] first tiles
+  __shared__ int s_wave[kSortThreads / 64];
+  const int buckets = p.adapters + 1;  // the last one: none
+  int* s_first = s_count + buckets;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int b = tid; b < buckets; b += kSortThreads) s_count[b] = 0;
+  __syncthreads();
+  auto bucket_of = [&](int t) {
+    const int a = t < p.tokens ? p.adapter[t] : -1;
+    return t >= p.tokens ? -1 : (a < 0 || a >= p.adapters ? p.adapters : a);
+  };
+  // Count the rows; place[t] is a row's place in its bucket.
+  for (int t0 = 0; t0 < p.tokens; t0 += kSortThreads * kSortAtOnce) {
+    int b[kSortAtOnce];
+#pragma unroll
+    for (int i = 0; i < kSortAtOnce; ++i) b[i] = bucket_of(t0 + i * kSortThreads + tid);
+#pragma unroll
+    for (int i = 0; i < kSortAtOnce; ++i) {
+      for (uint64_t todo = __ballot(b[i] >= 0); todo;) {
+        const int leader = (int)__builtin_ctzll(todo);
+        const int one = __builtin_amdgcn_readlane(b[i], leader);
+        const uint64_t own = __ballot(b[i] == one);
+        todo &= ~own;
+        int first = 0;
+        if (lane == leader) first = atomicAdd(&s_count[one], __popcll(own));
+        first = __builtin_amdgcn_readlane(first, leader);
+        if (b[i] == one)
+          p.place[t0 + i * kSortThreads + tid] =
+              first + __popcll(own & (((uint64_t)1 << lane) - 1));
+      }
+    }
+  }
+  __syncthreads();
+  // First tiles: sums of the buckets' tiles, a run of buckets per thread.
+  const int per = (buckets + kSortThreads - 1) / kSortThreads;
+  const int b0 = min(tid * per, buckets), b1 = min(b0 + per, buckets);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += (s_count[b] + kTileRows - 1) / kTileRows;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 63) s_wave[wave] = upto;
+  __syncthreads();
+  int first = upto - mine, all = 0;
+  for (int w = 0; w < kSortThreads / 64; ++w) {
+    if (w < wave) first += s_wave[w];
+    all += s_wave[w];
+  }
+  if (tid == 0) *p.tile_count = all;
+  for (int b = b0; b < b1; ++b) {
+    const int rows = s_count[b], tiles = (rows + kTileRows - 1) / kTileRows;
+    for (int i = rows; i < tiles * kTileRows; ++i) p.order[(int64_t)first * kTileRows + i] = -1;
+    s_first[b] = first;
+    first += tiles;
+  }
+  __syncthreads();
+#pragma unroll kSortAtOnce
+  for (int t = tid; t < p.tokens; t += kSortThreads) {
+    const int b = bucket_of(t), place = p.place[t];
+    const int tile = s_first[b] + place / kTileRows;
+    p.order[(int64_t)tile * kTileRows + place % kTileRows] = t;
+    if (place % kTileRows == 0) p.tiles[tile] = b < p.adapters ? b : -1;
+  }
 }
 
-// h of kDownRows rows, RT * 16 ranks and one chunk.  x and A pass through LDS, so
+// h of one tile's rows, RT * 16 ranks and one chunk.  x and A pass through LDS, so
 // that a wave loads two rows of 512 bytes at once: read straight into operands, 16
 // rows of 64 bytes whose stride is a multiple of 4 KiB fall on few cache sets and
 // channels.  Wave w contracts rows 16 (w%2) + (0..15) over half w/2 of each step.
@@ -298,88 +373,88 @@ template <int RT>
 __global__ __launch_bounds__(kThreads) void lora_down_tile_kernel(const LoraArgs p) {
   constexpr int kRow = kDownStep + 8;  // halves between rows in LDS
   constexpr int kRanks = RT * 16;
-  constexpr int kXLoads = kDownRows * kDownStep / 8 / kThreads;
+  constexpr int kXLoads = kTileRows * kDownStep / 8 / kThreads;
   constexpr int kALoads = kRanks * kDownStep / 8 / kThreads;
-  __shared__ __align__(16) uint16_t s_x[kDownRows * kRow];
+  __shared__ __align__(16) uint16_t s_x[kTileRows * kRow];
   __shared__ __align__(16) uint16_t s_a[kRanks * kRow];
-  __shared__ __align__(16) float s_h[kDownRows][kRanks + 4];  // of the second half
+  __shared__ __align__(16) float s_h[kTileRows][kRanks + 4];  // of the second half
+  const int tile = blockIdx.y;
+  if (tile >= *p.tile_count) return;
+  const int a = p.tiles[tile];
+  if (a < 0) return;
+  const int32_t* order = p.order + (int64_t)tile * kTileRows;
   const Site& s = site_of(p, false, blockIdx.x);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int m = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.y * kDownRows;
   const int rank_blocks = (s.rank + kRanks - 1) / kRanks;
   const int chunk = (blockIdx.x - s.first_down) / rank_blocks;
   const int j0 = (blockIdx.x - s.first_down) % rank_blocks * kRanks;
   const int ranks = min(kRanks, s.rank - j0);  // a multiple of 8
   const int c0 = chunk * s.chunk_cols, c1 = min(s.cols, c0 + s.chunk_cols);
-  const int id = adapter_of_lane(p, t0, kDownRows, lane);
-  // Thread tid stages 8 columns (tid % 32) of rows tid / 32 + 8 i.
+  // Thread tid stages 8 columns (tid % 32) of rows tid / 32 + 8 i; rows that are none
+  // stage the first one again.
   const int col = tid % (kDownStep / 8) * 8, row = tid / (kDownStep / 8);
   constexpr int kRowsAtOnce = kThreads / (kDownStep / 8);
-  const __half* x = static_cast<const __half*>(s.x);
-  uint64_t todo = __ballot(id >= 0);
-  while (todo) {
-    const int a = __builtin_amdgcn_readlane(id, (int)__ffsll((unsigned long long)todo) - 1);
-    const uint64_t own = __ballot(id == a);
-    todo &= ~own;
-    const __half* A = s.A + ((int64_t)a * s.rank + j0) * s.cols;
-    v4u xv[kXLoads], av[kALoads];
-    auto request = [&](int c) {
-      const v4u z = {0, 0, 0, 0};
-      const bool in = c + col < c1;
+  const __half* x[kXLoads];
 #pragma unroll
-      for (int i = 0; i < kXLoads; ++i) {
-        const int t = min(t0 + row + kRowsAtOnce * i, p.tokens - 1);
-        xv[i] = in ? *reinterpret_cast<const v4u*>(x + (int64_t)t * s.cols + c + col) : z;
-      }
+  for (int i = 0; i < kXLoads; ++i) {
+    const int t = order[row + kRowsAtOnce * i];
+    x[i] = static_cast<const __half*>(s.x) + (int64_t)(t >= 0 ? t : order[0]) * s.cols + col;
+  }
+  const __half* A = s.A + ((int64_t)a * s.rank + j0) * s.cols + col;
+  v4u xv[kXLoads], av[kALoads];
+  auto request = [&](int c) {
+    const v4u z = {0, 0, 0, 0};
+    const bool in = c + col < c1;
 #pragma unroll
-      for (int i = 0; i < kALoads; ++i) {
-        const int j = min(row + kRowsAtOnce * i, ranks - 1);
-        av[i] = in ? *reinterpret_cast<const v4u*>(A + (int64_t)j * s.cols + c + col) : z;
-      }
-    };
-    floatx4 acc[RT];
+    for (int i = 0; i < kXLoads; ++i) xv[i] = in ? *reinterpret_cast<const v4u*>(x[i] + c) : z;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
-    request(c0);
-    for (int c = c0; c < c1; c += kDownStep) {
-      __syncthreads();  // the step before has been read
-#pragma unroll
-      for (int i = 0; i < kXLoads; ++i)
-        *reinterpret_cast<v4u*>(&s_x[(row + kRowsAtOnce * i) * kRow + col]) = xv[i];
-#pragma unroll
-      for (int i = 0; i < kALoads; ++i)
-        *reinterpret_cast<v4u*>(&s_a[(row + kRowsAtOnce * i) * kRow + col]) = av[i];
-      if (c + kDownStep < c1) request(c + kDownStep);
-      __syncthreads();
-      const int k0 = (wave >> 1) * (kDownStep / 2) + g * 8;
-#pragma unroll
-      for (int k = 0; k < kDownStep / 2; k += 32) {
-        const v4u xk = *reinterpret_cast<const v4u*>(&s_x[((wave & 1) * 16 + m) * kRow + k0 + k]);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const v4u ak = *reinterpret_cast<const v4u*>(&s_a[(r * 16 + m) * kRow + k0 + k]);
-          acc[r] = mfma(ak, xk, acc[r]);
-        }
-      }
+    for (int i = 0; i < kALoads; ++i) {
+      const int j = min(row + kRowsAtOnce * i, ranks - 1);
+      av[i] = in ? *reinterpret_cast<const v4u*>(A + (int64_t)j * s.cols + c) : z;
     }
-    // the second half's sums pass to the first's waves, which hold the same rows
-    const int t = (wave & 1) * 16 + m;
-    if (wave >= 2) {
+  };
+  floatx4 acc[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) *reinterpret_cast<floatx4*>(&s_h[t][r * 16 + g * 4]) = acc[r];
-    }
+  for (int r = 0; r < RT; ++r) acc[r] = floatx4{0.f, 0.f, 0.f, 0.f};
+  request(c0);
+  for (int c = c0; c < c1; c += kDownStep) {
+    __syncthreads();  // the step before has been read
+#pragma unroll
+    for (int i = 0; i < kXLoads; ++i)
+      *reinterpret_cast<v4u*>(&s_x[(row + kRowsAtOnce * i) * kRow + col]) = xv[i];
+#pragma unroll
+    for (int i = 0; i < kALoads; ++i)
+      *reinterpret_cast<v4u*>(&s_a[(row + kRowsAtOnce * i) * kRow + col]) = av[i];
+    if (c + kDownStep < c1) request(c + kDownStep);
     __syncthreads();
-    if (wave < 2 && ((own >> t) & 1)) {
-      float* h = s.h + ((int64_t)chunk * p.tokens + t0 + t) * s.rank + j0;
+    const int k0 = (wave >> 1) * (kDownStep / 2) + g * 8;
+#pragma unroll
+    for (int k = 0; k < kDownStep / 2; k += 32) {
+      const v4u xk = *reinterpret_cast<const v4u*>(&s_x[((wave & 1) * 16 + m) * kRow + k0 + k]);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int j = r * 16 + g * 4;
-        if (j < ranks)
-          *reinterpret_cast<floatx4*>(h + j) =
-              acc[r] + *reinterpret_cast<const floatx4*>(&s_h[t][j]);
+        const v4u ak = *reinterpret_cast<const v4u*>(&s_a[(r * 16 + m) * kRow + k0 + k]);
+        acc[r] = mfma(ak, xk, acc[r]);
       }
     }
+  }
+  // the second half's sums pass to the first's waves, which hold the same rows
+  const int place = (wave & 1) * 16 + m;
+  if (wave >= 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) *reinterpret_cast<floatx4*>(&s_h[place][r * 16 + g * 4]) = acc[r];
+  }
+  __syncthreads();
+  const int t = order[place];
+  if (wave >= 2 || t < 0) return;
+  float* h = s.h + ((int64_t)chunk * p.tokens + t) * s.rank + j0;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int j = r * 16 + g * 4;
+    if (j < ranks)
+      *reinterpret_cast<floatx4*>(h + j) =
+          acc[r] + *reinterpret_cast<const floatx4*>(&s_h[place][j]);
   }
 }
 
@@ -389,106 +464,106 @@ __device__ v4u parts(v4u p0, v4u p1, uint32_t select) {
   return v4u{pick(p0[1], p0[0]), pick(p0[3], p0[2]), pick(p1[1], p1[0]), pick(p1[3], p1[2])};
 }
 
-// y of kUpRows rows and s.up_outputs outputs; wave w has rows 16 w + (0..15).  BLOCK:
-// ranks of a pass, 16 (for at most 16: high and low parts in one MFMA, B twice) or 32
-// (an MFMA each, on one load of B).
+// y of kUpRows rows (two tiles) and s.up_outputs outputs; a wave has 16 rows of one
+// tile, and nothing to do with the others.  BLOCK: ranks of a pass, 16 (for at most
+// 16: high and low parts in one MFMA, B twice) or 32 (an MFMA each, on one load of B).
 template <int BLOCK>
 __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p) {
   // h of the rows, each value as hi | lo << 16, ranks padded with zeros to BLOCKs;
   // the factor scales[a] * 2^e of each row; and a wave's sums of a step, turned over
   // so that base and y are read and written in runs of 256 bytes
-  extern __shared__ __align__(16) uint32_t s_pair[];
-  __shared__ float s_factor[kUpRows];
-  __shared__ __align__(16) float s_sum[kWaves][16][kUpStep + 4];
-  const Site& s = site_of(p, true, blockIdx.x);
+  extern __shared__ __align__(16) uint32_t s_all_pairs[];
+  __shared__ float s_all_factors[kUpRows];
+  __shared__ __align__(16) float s_all_sums[kWaves][16][kUpStep + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int m = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.y * kUpRows;
+  const int tile = blockIdx.y * (kUpRows / kTileRows) + wave / (kTileRows / 16);
+  if (tile >= *p.tile_count) return;
+  const Site& s = site_of(p, true, blockIdx.x);
+  const int a = __builtin_amdgcn_readfirstlane(p.tiles[tile]);
+  if (a < 0 && s.y == s.base) return;
+  const int32_t* order = p.order + (int64_t)tile * kTileRows + wave % (kTileRows / 16) * 16;
   const int ranks = (s.rank + BLOCK - 1) / BLOCK * BLOCK, stride = ranks + 4;
-  const int id = adapter_of_lane(p, t0, kUpRows, lane);
-  const int r0 = wave * 16;  // the wave's rows, but in the next block
-  const bool copies = s.y != s.base;
-  const uint32_t has = (uint32_t)(__ballot(id >= 0) >> r0) & 0xFFFF;
-  // This lane's 8 ranks of a block, and which parts: all high ones, or with BLOCK 16
-  // the low ones for the upper half of the lanes.
-  const int at = BLOCK == 16 ? (g & 1) * 8 : g * 8;
-  const uint32_t high = 0x05040100u, low = 0x07060302u;
-  const uint32_t select = BLOCK == 16 && g >= 2 ? low : high;
+  uint32_t* s_pair = s_all_pairs + wave * 16 * stride;
+  float* s_factor = s_all_factors + wave * 16;
+  auto& s_sum = s_all_sums[wave];
+  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows order[4 i + l/16].
   const int o_begin = (blockIdx.x - s.first_up) * s.up_outputs;
   const int o_end = min(s.rows, o_begin + s.up_outputs);
-  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows 4 i + l/16.
-  const __half* base = static_cast<const __half*>(s.base) + (int64_t)(t0 + r0) * s.rows + m * 8;
-  __half* y = static_cast<__half*>(s.y) + (int64_t)(t0 + r0) * s.rows + m * 8;
+  int rows[4];
   v4u bases[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rows[i] = order[4 * i + g];
   auto request = [&](int o0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens)
+      if (o0 + m * 8 < s.rows && rows[i] >= 0)
         bases[i] = __builtin_nontemporal_load(
-            reinterpret_cast<const v4u*>(base + (int64_t)(4 * i + g) * s.rows + o0));
+            reinterpret_cast<const v4u*>(static_cast<const __half*>(s.base) +
+                                         (int64_t)rows[i] * s.rows + o0 + m * 8));
   };
-  const bool done = t0 + r0 >= p.tokens || (has == 0 && !copies);
-  if (!done) request(o_begin);
-  {
-    // four threads a row, four ranks at a time
+  request(o_begin);
+  if (a >= 0) {
+    // four lanes a row, four ranks at a time
     constexpr int kAtOnce = 8;
-    const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
-    const int a = __shfl(id, t);
+    const int part = lane & 3, t = max(order[lane >> 2], 0);
+    uint32_t* pair = s_pair + (lane >> 2) * stride;
     float top = 0.f;
-    if (a >= 0) {
 #pragma unroll 2
-      for (int j = part * 4; j < ranks; j += 16) {
-        floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int c0 = 0; j < s.rank && c0 < s.chunks; c0 += kAtOnce) {
-          floatx4 v[kAtOnce];  // requested together
+    for (int j = part * 4; j < ranks; j += 16) {
+      floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+      for (int c0 = 0; j < s.rank && c0 < s.chunks; c0 += kAtOnce) {
+        floatx4 v[kAtOnce];  // requested together
 #pragma unroll
-          for (int c = 0; c < kAtOnce; ++c) {
-            v[c] = floatx4{0.f, 0.f, 0.f, 0.f};
-            if (c0 + c < s.chunks)
-              v[c] = *reinterpret_cast<const floatx4*>(
-                  s.h + ((int64_t)(c0 + c) * p.tokens + t0 + t) * s.rank + j);
-          }
-#pragma unroll
-          for (int c = 0; c < kAtOnce; ++c) sum += v[c];
+        for (int c = 0; c < kAtOnce; ++c) {
+          v[c] = floatx4{0.f, 0.f, 0.f, 0.f};
+          if (c0 + c < s.chunks)
+            v[c] = *reinterpret_cast<const floatx4*>(
+                s.h + ((int64_t)(c0 + c) * p.tokens + t) * s.rank + j);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(sum[i]));
-        *reinterpret_cast<floatx4*>(&s_pair[t * stride + j]) = sum;
+        for (int c = 0; c < kAtOnce; ++c) sum += v[c];
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(sum[i]));
+      *reinterpret_cast<floatx4*>(&pair[j]) = sum;
     }
     top = fmaxf(top, __shfl_xor(top, 1));
     top = fmaxf(top, __shfl_xor(top, 2));
     // the row's largest value into [2^9, 2^10): the low parts keep all bits
     int e = 10;
     if (top > 0.f && top < INFINITY) (void)frexpf(top, &e);
-    if (a >= 0) {
-      for (int j = part * 4; j < ranks; j += 16) {
-        v4u* at = reinterpret_cast<v4u*>(&s_pair[t * stride + j]);
-        v4u v = *at;
+    for (int j = part * 4; j < ranks; j += 16) {
+      v4u* at = reinterpret_cast<v4u*>(&pair[j]);
+      v4u v = *at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = ldexpf(__uint_as_float(v[i]), 10 - e);
-          const _Float16 hi = (_Float16)f, lo = (_Float16)(f - (float)hi);
-          v[i] = __builtin_bit_cast(uint16_t, hi) |
-                 (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
-        }
-        *at = v;
+      for (int i = 0; i < 4; ++i) {
+        const float f = ldexpf(__uint_as_float(v[i]), 10 - e);
+        const _Float16 hi = (_Float16)f, lo = (_Float16)(f - (float)hi);
+        v[i] = __builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
       }
-      if (part == 0) s_factor[t] = ldexpf(p.scales[a], e - 10);
+      *at = v;
     }
+    if (part == 0) s_factor[lane >> 2] = ldexpf(p.scales[a], e - 10);
   }
-  __syncthreads();
-  if (done) return;
+  // a wave's own LDS accesses stay in order
+  auto settle = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  settle();
+  // This lane's 8 ranks of a block, and which parts: all high ones, or with BLOCK 16
+  // the low ones for the upper half of the lanes.
+  const int at = BLOCK == 16 ? (g & 1) * 8 : g * 8;
+  const uint32_t high = 0x05040100u, low = 0x07060302u;
+  const uint32_t select = BLOCK == 16 && g >= 2 ? low : high;
+  const __half* B = s.B + (int64_t)max(a, 0) * s.rows * s.rank + at;
+  __half* y = static_cast<__half*>(s.y);
   for (int o0 = o_begin; o0 < o_end; o0 += kUpStep) {
-    uint32_t todo = has;
-    while (todo) {
-      const int a = __builtin_amdgcn_readlane(id, r0 + __ffs(todo) - 1);
-      const uint32_t own = (uint32_t)(__ballot(id == a) >> r0) & 0xFFFF;
-      todo &= ~own;
+    if (a >= 0) {
       floatx4 acc[kUpStep / 16];
 #pragma unroll
       for (int u = 0; u < kUpStep / 16; ++u) acc[u] = floatx4{0.f, 0.f, 0.f, 0.f};
-      const __half* B = s.B + (int64_t)a * s.rows * s.rank + at;
       for (int j = 0; j < ranks; j += BLOCK) {
         v4u bv[kUpStep / 16];
 #pragma unroll
@@ -498,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
           if (j + at < s.rank)
             bv[u] = *reinterpret_cast<const v4u*>(B + (int64_t)o * s.rank + j);
         }
-        const uint32_t* pair = &s_pair[(r0 + m) * stride + j + at];
+        const uint32_t* pair = &s_pair[m * stride + j + at];
         const v4u p0 = *reinterpret_cast<const v4u*>(pair);
         const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
         const v4u hv = parts(p0, p1, select);
@@ -510,22 +585,18 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
           for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], lv, acc[u]);
         }
       }
-      if ((own >> m) & 1) {
-        const float f = s_factor[r0 + m];
+      const float f = s_factor[m];
 #pragma unroll
-        for (int u = 0; u < kUpStep / 16; ++u)
-          *reinterpret_cast<floatx4*>(&s_sum[wave][m][16 * u + 4 * g]) = f * acc[u];
-      }
+      for (int u = 0; u < kUpStep / 16; ++u)
+        *reinterpret_cast<floatx4*>(&s_sum[m][16 * u + 4 * g]) = f * acc[u];
     }
-    // the wave's own part of s_sum: its LDS accesses stay in order
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    settle();
     v4u out[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       out[i] = bases[i];
-      if (!((has >> (4 * i + g)) & 1)) continue;
-      const float* sum = &s_sum[wave][4 * i + g][m * 8];
+      if (a < 0) continue;
+      const float* sum = &s_sum[4 * i + g][m * 8];
       const floatx4 lo = *reinterpret_cast<const floatx4*>(sum);
       const floatx4 hi = *reinterpret_cast<const floatx4*>(sum + 4);
       const __half* b = reinterpret_cast<const __half*>(&bases[i]);
@@ -534,14 +605,12 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
       for (int k = 0; k < 8; ++k)
         q[k] = __float2half_rn(__half2float(b[k]) + (k < 4 ? lo[k & 3] : hi[k & 3]));
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    settle();
     if (o0 + kUpStep < o_end) request(o0 + kUpStep);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (o0 + m * 8 < s.rows && t0 + r0 + 4 * i + g < p.tokens &&
-          (copies || (has >> (4 * i + g)) & 1))
-        *reinterpret_cast<v4u*>(y + (int64_t)(4 * i + g) * s.rows + o0) = out[i];
+      if (o0 + m * 8 < s.rows && rows[i] >= 0)
+        *reinterpret_cast<v4u*>(y + (int64_t)rows[i] * s.rows + o0 + m * 8) = out[i];
   }
 }
 
@@ -557,14 +626,14 @@ bool wide_site(const seedlm_lora_site& s) {
 // How the sites [0, n) of one group run.
 enum Kind { kOne, kRows, kTiles };
 
-// Tiles need rows enough to fill them and products enough to repay their set-up.
-// GPU time of a call, tiles against rows, 8 requests of one adapter each: q, k and v
-// of a 70B layer at rank 16 14.1 and 12.1 us at 64 rows, 11.4 and 21 at 128; gate and
-// up of an 8B layer at rank 64 31 and 41 us at 64, 28 and 76 at 128; 512 x 512 at rank
-// 16 (17 MB at 512 rows) 8.0 and 6.9 at 512.  Rows that alternate among 16 adapters
-// cost the tiles more: 42 against 12 us for the first at 64 rows, 67 and 66 at 512.
+// Tiles need rows enough to fill them and products enough to repay the sort and the
+// set-up.  GPU time of a call, tiles against rows, all rows of one adapter (and rows
+// alternating among 16): q, k and v of a 70B layer at rank 16, 96 rows (107 MB) 13.4
+// (21) and 16 us, 128 rows 13.6 (21) and 21; gate and up of an 8B layer at rank 64, 64
+// rows (302 MB) 18 (47) and 36 (46), 128 rows 21 (47) and 69 (88); 4096 x 11008 at rank
+// 32, 96 rows (93 MB) 15.4 (20) and 13.
 constexpr int64_t kTileTokens = 64;
-constexpr int64_t kTileBytes = 64 << 20;  // A and B, once per row
+constexpr int64_t kTileBytes = 128 << 20;  // A and B, once per row
 // One launch pays while A is small for a workgroup to read whole and the workgroups
 // are at most the compute units (every one reads A).  One launch against two: q, k
 // and v of a 70B layer at rank 16 7.2 and 7.8 us at 16 rows, 9.0 and 12.0 at 64; gate
@@ -584,9 +653,10 @@ int one_outputs(const seedlm_lora_site* s, int n, int64_t tokens, int64_t* workg
   }
 }
 
-Kind kind_of(const seedlm_lora_site* s, int n, int64_t tokens, int xdt, int ydt) {
+Kind kind_of(const seedlm_lora_site* s, int n, int64_t tokens, int adapters, int xdt, int ydt) {
   int64_t bytes = 0, workgroups = 0;
-  bool one = true, tile = tokens >= kTileTokens && xdt == SEEDLM_F16 && ydt == SEEDLM_F16;
+  bool one = true, tile = tokens >= kTileTokens && xdt == SEEDLM_F16 && ydt == SEEDLM_F16 &&
+                          adapters <= kSortAdapters;
   for (int i = 0; i < n; ++i) {
     bytes += tokens * s[i].rank * (s[i].rows + s[i].cols) * 2;
     one = one && s[i].rank <= kOneRank && s[i].rank * s[i].cols * 2 <= kOneBytes;
@@ -604,7 +674,7 @@ Kind kind_of(const seedlm_lora_site* s, int n, int64_t tokens, int xdt, int ydt)
 // their sums (128 where few rows leave few such workgroups).
 int chunk_cols_of(const seedlm_lora_site& s, int n, int64_t tokens, Kind kind) {
   if (kind != kTiles) return kChunk;
-  const int64_t across = (tokens + kDownRows - 1) / kDownRows * n;
+  const int64_t across = (tokens + kTileRows - 1) / kTileRows * n;
   int64_t chunks = (4 * device_cu_count() + across - 1) / across;
   const int64_t sums = tokens <= 2 * kUpRows ? 512 : 256;
   for (int64_t most : {(s.cols + 511) / 512, sums / s.rank})
@@ -631,6 +701,16 @@ int up_outputs_of(const seedlm_lora_site& s, int n, int64_t tokens, int chunks) 
   return (int)(each < 1 ? 1 : each) * kUpStep;
 }
 
+// Tiles at most: each adapter, and the rows without one, may leave one part-filled.
+int64_t tiles_most(int64_t tokens, int adapters) {
+  const int64_t some = tokens < adapters + 1 ? tokens : adapters + 1;
+  return (tokens + kTileRows - 1) / kTileRows + some;
+}
+// Scratch of the tiles: their number, adapters and rows, and the rows' places.
+int64_t tile_floats(int64_t tokens, int adapters) {
+  return (64 + tiles_most(tokens, adapters) * (1 + kTileRows) + tokens + 63) / 64 * 64;
+}
+
 int group_size(int n, int i) { return n - i < kLoraGroup ? n - i : kLoraGroup; }
 
 template <typename XT, typename YT>
@@ -650,12 +730,13 @@ void run_rows(const LoraArgs& p, int down, int up, hipStream_t s) {
 }  // namespace
 
 // The groups run one after another and share the scratch of the largest.
-size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int xdt, int ydt) {
+size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int adapters,
+                          int xdt, int ydt) {
   size_t most = 0;
   for (int i = 0; i < n; i += kLoraGroup) {
     const int k = group_size(n, i);
-    const Kind kind = kind_of(sites + i, k, tokens, xdt, ydt);
-    size_t floats = 0;
+    const Kind kind = kind_of(sites + i, k, tokens, adapters, xdt, ydt);
+    size_t floats = kind == kTiles ? tile_floats(tokens, adapters) : 0;
     for (int j = i; j < i + k && kind != kOne; ++j)
       floats += site_floats(sites[j], chunk_cols_of(sites[j], k, tokens, kind), tokens);
     if (floats > most) most = floats;
@@ -672,9 +753,17 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
     p.scales = scales;
     p.tokens = (int)tokens;
     p.adapters = adapters;
-    const Kind kind = kind_of(sites + i, p.n, tokens, xdt, ydt);
+    const Kind kind = kind_of(sites + i, p.n, tokens, adapters, xdt, ydt);
     const bool tile = kind == kTiles;
+    const int64_t tiles = tiles_most(tokens, adapters);
     float* h = scratch;
+    if (tile) {
+      p.tile_count = reinterpret_cast<int32_t*>(scratch);
+      p.tiles = p.tile_count + 64;
+      p.order = p.tiles + tiles;
+      p.place = p.order + tiles * kTileRows;
+      h += tile_floats(tokens, adapters);
+    }
     int top_rank = 0;
     for (int k = 0; k < p.n; ++k)
       if (sites[i + k].rank > top_rank) top_rank = sites[i + k].rank;
@@ -716,8 +805,10 @@ int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, co
         else run_one<float, float>(p, up, s);
       }
     } else if (tile) {
-      const dim3 dg(down, (p.tokens + kDownRows - 1) / kDownRows);
-      const dim3 ug(up, (p.tokens + kUpRows - 1) / kUpRows);
+      const int buckets = adapters + 1;
+      hipLaunchKernelGGL(lora_sort_kernel, dim3(1), dim3(kSortThreads),
+                         2 * buckets * sizeof(int), s, p);
+      const dim3 dg(down, tiles), ug(up, (tiles + kUpRows / kTileRows - 1) / (kUpRows / kTileRows));
       const auto down_kernel = rank_tiles == 1   ? lora_down_tile_kernel<1>
                                : rank_tiles == 2 ? lora_down_tile_kernel<2>
                                                  : lora_down_tile_kernel<kDownRanks / 16>;

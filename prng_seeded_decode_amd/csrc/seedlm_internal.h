@@ -172,7 +172,8 @@ int launch_cache_append(const seedlm_cache_append_args& a, hipStream_t s);
 size_t cache_attend_scratch_bytes(const seedlm_cache_attend_args& a);
 int launch_cache_attend(const seedlm_cache_attend_args& a, void* scratch, hipStream_t s);
 constexpr int kLoraGroup = 8;  // sites of one pair of launches
-size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int xdt, int ydt);
+size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int adapters,
+                          int xdt, int ydt);
 int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, const float* scales,
                 int64_t tokens, int adapters, int xdt, int ydt, float* scratch, hipStream_t s);
 

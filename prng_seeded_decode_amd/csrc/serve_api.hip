@@ -197,18 +197,18 @@ int seedlm_lora_many(const seedlm_lora_site* sites, int n, const int32_t* adapte
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   void* scratch = nullptr;
-  st = scratch_for(s, lora_scratch_bytes(sites, n, tokens, x_dtype, y_dtype), &scratch);
+  st = scratch_for(s, lora_scratch_bytes(sites, n, tokens, adapters, x_dtype, y_dtype), &scratch);
   if (st != SEEDLM_OK) return st;
   return launch_lora(sites, n, adapter, scales, tokens, adapters, x_dtype, y_dtype,
                      static_cast<float*>(scratch), s);
 }
 
-int seedlm_lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int x_dtype,
-                              int y_dtype, size_t* bytes) {
-  if (!bytes) return SEEDLM_E_INVALID;
+int seedlm_lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int adapters,
+                              int x_dtype, int y_dtype, size_t* bytes) {
+  if (!bytes || adapters < 1) return SEEDLM_E_INVALID;
   const int st = check_lora_sizes(sites, n, tokens, x_dtype, y_dtype);
   if (st != SEEDLM_OK) return st;
-  *bytes = lora_scratch_bytes(sites, n, tokens, x_dtype, y_dtype);
+  *bytes = lora_scratch_bytes(sites, n, tokens, adapters, x_dtype, y_dtype);
   return SEEDLM_OK;
 }
 

@@ -92,10 +92,10 @@ def test_lora_of_few_rows(tokens, rank, sites, kind, x16, y16):
     (129, 64, [(72, 1096)]), (200, 16, [(1024, 1024), (256, 1024), (256, 1024)]),
     (77, 24, [(520, 264)]), (130, 128, [(136, 264)]), (50, 256, [(200, 136)]),
     (40, 5, [(33, 47)]), (65, 20, [(130, 100)]), (35, 16, [(8, 8)]), (257, 48, [(328, 2056)]),
-    # enough products for the matrix cores (64 MB of A and B, counted once per row)
-    (513, 16, [(2056, 2064)]), (129, 256, [(520, 520)]), (300, 64, [(904, 1000)]),
-    (700, 24, [(1032, 968)]), (1030, 8, [(2056, 2056), (264, 2056)]), (200, 128, [(680, 680)]),
-    (2100, 16, [(1000, 1000)]), (64, 240, [(1608, 600)]), (350, 32, [(8, 3000)]),
+    # enough products for the matrix cores (128 MiB of A and B, counted once per row)
+    (1030, 16, [(2056, 2064)]), (129, 256, [(1032, 1032)]), (300, 64, [(1800, 1720)]),
+    (700, 24, [(2056, 1944)]), (1030, 8, [(4104, 2056), (264, 2056)]), (400, 128, [(680, 680)]),
+    (4200, 16, [(1000, 1000)]), (64, 240, [(3208, 1200)]), (700, 32, [(8, 3000)]),
 ])
 def test_lora_of_many_rows(tokens, rank, sites, kind):
     c = make([tokens, rank, 1], sites, rank, tokens, 5, ids_of([tokens], tokens, 5, kind))
@@ -119,7 +119,7 @@ def test_lora_of_more_sites_than_one_launch_takes():
 
 
 # one launch, the row kernels, the matrix cores
-FORMS = [(6, 16, (264, 512)), (96, 24, (264, 512)), (170, 64, (1032, 2056))]
+FORMS = [(6, 16, (264, 512)), (96, 24, (264, 512)), (340, 64, (1032, 2056))]
 
 
 @pytest.mark.parametrize("tokens,rank,site", FORMS)
@@ -210,3 +210,15 @@ def test_lora_beside_a_packed_projection():
     got = base.double().cpu().numpy()
     assert np.linalg.norm(got - ref) <= 2e-3 * np.linalg.norm(ref)
     m.destroy()
+
+
+@pytest.mark.parametrize("adapters,tokens,rank,site", [
+    (300, 2100, 16, (1000, 1048)), (8191, 16100, 8, (520, 8)), (8200, 16100, 8, (520, 8))])
+def test_lora_of_many_adapters(adapters, tokens, rank, site):
+    # tiles of a row or two each, and more adapters than the sort takes
+    rng = np.random.default_rng(adapters)
+    ids = rng.integers(-1, adapters + 1, tokens)
+    ids[: tokens // 3] = 7
+    c = make([28, adapters], [site], rank, tokens, adapters, ids)
+    check(c, run(c))
+    check(c, run(c, in_place=True))

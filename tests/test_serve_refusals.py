@@ -151,12 +151,13 @@ def test_lora_scratch_is_the_largest_groups():
     arr = (V._LoraSite * 17)(*[V._LoraSite(P, P, P, P, P, 64, 32, 32)] * 17)
 
     def ask(k):
-        assert S.lib().seedlm_lora_scratch_bytes(ctypes.cast(arr, ctypes.c_void_p), k, 4, 1, 1,
+        assert S.lib().seedlm_lora_scratch_bytes(ctypes.cast(arr, ctypes.c_void_p), k, 4, 2, 1, 1,
                                                  ctypes.byref(n)) == S.OK
         return n.value
 
     assert ask(0) == 0 and 0 < ask(1) < ask(8) == ask(17)
-    assert S.lib().seedlm_lora_scratch_bytes(None, 1, 4, 1, 1, ctypes.byref(n)) == S.E_INVALID
+    assert S.lib().seedlm_lora_scratch_bytes(None, 1, 4, 2, 1, 1, ctypes.byref(n)) == S.E_INVALID
+    assert S.lib().seedlm_lora_scratch_bytes(None, 0, 4, 0, 1, 1, ctypes.byref(n)) == S.E_INVALID
 
 
 def test_python_wrappers_refuse_what_does_not_fit():
