@@ -209,8 +209,9 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  *   adapter  device int32 [tokens], in any order; a value outside
  *          [0, adapters) means none: y_i[t] = base_i[t]
  *   scales device fp32 [adapters]
- * rank in [1, SEEDLM_MAX_RANK] per site; n sites, up to 8 consecutive ones in
- * one pair of launches.  x_dtype and y_dtype are SEEDLM_F32 or SEEDLM_F16.
+ * rank in [1, SEEDLM_MAX_RANK] per site; n sites, up to 8 consecutive ones
+ * sharing their launches: one for few rows with a small A, two, or three for
+ * many rows.  x_dtype and y_dtype are SEEDLM_F32 or SEEDLM_F16.
  * A row's result depends on its own adapter alone: NaN or infinities in other
  * adapters do not reach it.  A x is held in fp32; the sum is rounded once.
  * Calls with fp16 x and y and many rows run on the matrix cores, A x entering

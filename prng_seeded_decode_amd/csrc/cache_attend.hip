@@ -36,6 +36,13 @@
 // fp16 numbers, which keeps 22 bits; one fp16 number alone would add as much
 // error as the rounding of an fp16 output does.  fp32 queries are split alike,
 // after scaling each row by a power of two.
+//
+// Measured (main launch, then the join; a streaming read reaches 6.2 TB/s): one
+// request of 131071 tokens of 8 cache heads, 128 dimensions, 537 MB, 97 + 4.7 us, 5.5
+// TB/s, reading 541 MB; 64 ragged requests of up to 16384 tokens, 2.15 GB, 371 + 5.8
+// us, 5.8 TB/s; 16 of up to 8192, 269 MB, 51 + 4.6 us.  Matrix cores are busy 5% of the
+// time and vector units 13%: what is left is the start of each run (lengths, page
+// numbers, first keys: 7 to 9 us before the reads are at full rate) and its end.
 #include <hip/hip_fp16.h>
 
 #include <type_traits>

@@ -22,6 +22,10 @@
 //         largest |h|); up to rank 16 the 16 high and 16 low parts fill the 32
 //         products of one MFMA against the same 16 elements of B twice.
 // The bytes of x, base and y bound these.
+//
+// Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 9.3 us in
+// one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.4, down 10.2,
+// up 54.5 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call.
 #include <hip/hip_fp16.h>
 
 #include "seedlm_internal.h"
@@ -52,7 +56,7 @@ struct Site {
   int rows, cols, rank;
   int chunks;
   int chunk_cols; // columns of a chunk
-  int up_outputs; // outputs of an up workgroup of the tile kernels
+  int up_outputs; // outputs of an up workgroup
   int wide;       // 16-byte accesses fit
   int first_down; // first workgroup (x dimension) of this site in the two launches
   int first_up;
