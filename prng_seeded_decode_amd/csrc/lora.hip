@@ -23,7 +23,7 @@
 //         products of one MFMA against the same 16 elements of B twice.
 // The bytes of x, base and y bound these.
 //
-// Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 9.3 us in
+// Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 8.0 us in
 // one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.4, down 10.2,
 // up 54.5 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call.
 #include <hip/hip_fp16.h>
@@ -233,6 +233,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_rows_kernel(const LoraArgs p
 // ---- fewest rows: one launch ----
 
 constexpr int kOneThreads = 1024;
+constexpr int kOneRank = 16;  // ranks at most
 constexpr int kOneWaves = kOneThreads / 64;
 
 // y of one token and a block of outputs of one site, h included: every workgroup of
@@ -240,8 +241,8 @@ constexpr int kOneWaves = kOneThreads / 64;
 // second launch while the repeated reads of A are few.
 template <typename XT, typename YT>
 __global__ __launch_bounds__(kOneThreads) void lora_one_kernel(const LoraArgs p, int blocks) {
-  __shared__ float s_part[kOneWaves][16];
-  __shared__ float s_h[SEEDLM_MAX_RANK];
+  __shared__ float s_part[kOneWaves][kOneRank];
+  __shared__ float s_h[kOneRank];
   // 8 tokens or more: a token's workgroups take one XCD (block number mod 8), whose
   // L2 then serves the repeats
   const int padded = (p.tokens + 7) / 8 * 8;
@@ -254,33 +255,49 @@ __global__ __launch_bounds__(kOneThreads) void lora_one_kernel(const LoraArgs p,
   const bool has = a >= 0 && a < p.adapters;
   if (!has && s.y == s.base) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int first = (block - s.first_up) * s.up_outputs;
+  const int end = min(s.rows, first + s.up_outputs);
+  const YT* base = static_cast<const YT*>(s.base) + (int64_t)t * s.rows;
+  YT* y = static_cast<YT*>(s.y) + (int64_t)t * s.rows;
+  // What the thread's first output needs, requested before A x.
+  const int mine = first + tid;
+  const float base0 = mine < end ? (float)base[mine] : 0.f;
+  const bool ahead = has && s.wide && mine < end;
+  half8 b_lo = {0, 0, 0, 0, 0, 0, 0, 0}, b_hi = b_lo;
+  if (ahead) {
+    const half8* B = reinterpret_cast<const half8*>(s.B + ((int64_t)a * s.rows + mine) * s.rank);
+    b_lo = B[0];
+    if (s.rank > 8) b_hi = B[1];
+  }
   if (has) {
-    const XT* x = static_cast<const XT*>(s.x) + (int64_t)t * s.cols;
-    const __half* A = s.A + (int64_t)a * s.rank * s.cols;
-    for (int j0 = 0; j0 < s.rank; j0 += 16) {
-      const int ranks = min(16, s.rank - j0);
-      float v[16];
-      contract16<kOneThreads>(x, A + (int64_t)j0 * s.cols, s.cols, ranks, s.wide, 0, s.cols, v);
-      const float sum = wave_sums16(v);
-      __syncthreads();  // s_part has been read
-      if ((lane & 3) == 0) s_part[wave][lane >> 2] = sum;
-      __syncthreads();
-      if (tid < ranks) {
-        float h = 0.f;
+    float v[16];
+    contract16<kOneThreads>(static_cast<const XT*>(s.x) + (int64_t)t * s.cols,
+                            s.A + (int64_t)a * s.rank * s.cols, s.cols, s.rank, s.wide, 0, s.cols,
+                            v);
+    const float sum = wave_sums16(v);
+    if ((lane & 3) == 0) s_part[wave][lane >> 2] = sum;
+    __syncthreads();
+    if (tid < kOneRank) {
+      float h = 0.f;
 #pragma unroll
-        for (int w = 0; w < kOneWaves; ++w) h += s_part[w][tid];
-        s_h[j0 + tid] = h * p.scales[a];
-      }
+      for (int w = 0; w < kOneWaves; ++w) h += s_part[w][tid];
+      s_h[tid] = tid < s.rank ? h * p.scales[a] : 0.f;
     }
     __syncthreads();
   }
-  const int first = (block - s.first_up) * s.up_outputs;
-  const int end = min(s.rows, first + s.up_outputs);
   for (int r = first + tid; r < end; r += kOneThreads) {
-    const int64_t at = (int64_t)t * s.rows + r;
-    float sum = (float)static_cast<const YT*>(s.base)[at];
-    if (has) sum += dot_b(s, a, r, s_h);
-    static_cast<YT*>(s.y)[at] = (YT)sum;
+    float sum = r == mine ? base0 : (float)base[r], d = 0.f;
+    if (ahead && r == mine) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d = fmaf((float)b_lo[i], s_h[i], d);
+      if (s.rank > 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d = fmaf((float)b_hi[i], s_h[8 + i], d);
+      }
+    } else if (has) {
+      d = dot_b(s, a, r, s_h);
+    }
+    y[r] = (YT)(sum + d);
   }
 }
 
@@ -640,12 +657,10 @@ constexpr int64_t kTileTokens = 64;
 constexpr int64_t kTileBytes = 128 << 20;  // A and B, once per row
 // One launch pays while A is small for a workgroup to read whole and the workgroups
 // are at most the compute units (every one reads A).  One launch against two: q, k
-// and v of a 70B layer at rank 16 7.2 and 7.8 us at 16 rows, 9.0 and 12.0 at 64; gate
-// and up of an 8B layer 5.7 and 6.5 at 1, 7.8 and 9.9 at 32 (256 workgroups), 13.8
-// and 13.5 at 64; 512 x 512 4.8 and 5.8 at 1; 8192 x 28672 10.8 and 8.5; at rank 32 (two
-// turns) 4096 x 11008 11.9 and 7.9.
+// and v of a 70B layer at rank 16 6.7 and 7.8 us at 16 rows, 9.0 and 12.0 at 64; gate
+// and up of an 8B layer 5.0 and 6.5 at 1, 7.7 and 9.9 at 32 (256 workgroups), 13.8
+// and 13.5 at 64; 512 x 512 3.9 and 5.8 at 1; 8192 x 28672 10.8 and 8.5.
 constexpr int64_t kOneBytes = 256 << 10;  // of one adapter's A
-constexpr int kOneRank = 16;
 
 // Outputs of a workgroup of lora_one_kernel: a row per thread, or up to four where
 // there are more workgroups than compute units; *workgroups gets their number.
