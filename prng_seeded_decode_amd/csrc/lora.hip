@@ -17,15 +17,16 @@
 //   sort  rows gathered by adapter into tiles of 32, so that a tile has one adapter
 //         however the rows lie
 //   down  a tile and up to 64 ranks per workgroup, x and A staged through LDS
-//   up    16 rows and 128 outputs per wave and step; the sums turn over in LDS.  h
+//   up    a tile and 64 outputs per wave and step; the sums turn over in LDS.  h
 //         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
 //         largest |h|); up to rank 16 the 16 high and 16 low parts fill the 32
 //         products of one MFMA against the same 16 elements of B twice.
 // The bytes of x, base and y bound these.
 //
 // Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 8.0 us in
-// one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.4, down 10.2,
-// up 54.5 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call.
+// one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.6, down 10.0,
+// up 55 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call; 1159 rows on
+// q, k and v of the 70B layer at rank 64, sort 4.9, down 19, up 30 us.
 #include <hip/hip_fp16.h>
 
 #include "seedlm_internal.h"
@@ -39,8 +40,9 @@ constexpr int kChunk = 8 * kThreads;  // columns of a workgroup of the row kerne
 constexpr int kTileRows = 32;    // rows of a tile, of one adapter
 constexpr int kDownRanks = 64;   // ranks at most of a down workgroup
 constexpr int kDownStep = 256;   // columns staged at once
-constexpr int kUpRows = 16 * kWaves;  // rows of an up workgroup, 16 per wave
-constexpr int kUpStep = 128;          // outputs of a wave's step
+constexpr int kUpRows = 2 * kTileRows;  // rows of an up workgroup, two waves per tile
+constexpr int kUpStep = 128;            // outputs of its step
+static_assert(kWaves == 4, "the tile kernels share tiles out to four waves");
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -485,50 +487,54 @@ __device__ v4u parts(v4u p0, v4u p1, uint32_t select) {
   return v4u{pick(p0[1], p0[0]), pick(p0[3], p0[2]), pick(p1[1], p1[0]), pick(p1[3], p1[2])};
 }
 
-// y of kUpRows rows (two tiles) and s.up_outputs outputs; a wave has 16 rows of one
-// tile, and nothing to do with the others.  BLOCK: ranks of a pass, 16 (for at most
-// 16: high and low parts in one MFMA, B twice) or 32 (an MFMA each, on one load of B).
+// y of two tiles' rows and s.up_outputs outputs; of a step, a wave has its tile's rows
+// and 64 outputs, so that B is loaded once for 32 rows (the vector cache's accesses
+// bound higher ranks).  BLOCK: ranks of a pass, 16 (for at most 16: high and low parts
+// in one MFMA, B twice) or 32 (an MFMA each, on one load of B).
 template <int BLOCK>
 __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p) {
+  constexpr int kOut = kUpStep / 2;  // outputs of a wave's step
   // h of the rows, each value as hi | lo << 16, ranks padded with zeros to BLOCKs;
   // the factor scales[a] * 2^e of each row; and a wave's sums of a step, turned over
-  // so that base and y are read and written in runs of 256 bytes
+  // so that base and y are read and written in runs of 128 bytes
   extern __shared__ __align__(16) uint32_t s_all_pairs[];
   __shared__ float s_all_factors[kUpRows];
-  __shared__ __align__(16) float s_all_sums[kWaves][16][kUpStep + 4];
+  __shared__ __align__(16) float s_all_sums[kWaves][kTileRows][kOut + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.y * (kUpRows / kTileRows) + wave / (kTileRows / 16);
-  if (tile >= *p.tile_count) return;
+  const int m = lane & 15, g = lane >> 4, half = wave & 1;
+  const int tiles = *p.tile_count;
+  if ((int)blockIdx.y * 2 >= tiles) return;
   const Site& s = site_of(p, true, blockIdx.x);
+  const int tile = min((int)blockIdx.y * 2 + (wave >> 1), tiles - 1);
   const int a = __builtin_amdgcn_readfirstlane(p.tiles[tile]);
-  if (a < 0 && s.y == s.base) return;
-  const int32_t* order = p.order + (int64_t)tile * kTileRows + wave % (kTileRows / 16) * 16;
+  const bool idle = (int)blockIdx.y * 2 + (wave >> 1) >= tiles || (a < 0 && s.y == s.base);
+  const int32_t* order = p.order + (int64_t)tile * kTileRows;
   const int ranks = (s.rank + BLOCK - 1) / BLOCK * BLOCK, stride = ranks + 4;
-  uint32_t* s_pair = s_all_pairs + wave * 16 * stride;
-  float* s_factor = s_all_factors + wave * 16;
+  uint32_t* s_pair = s_all_pairs + (wave >> 1) * kTileRows * stride;
+  float* s_factor = s_all_factors + (wave >> 1) * kTileRows;
   auto& s_sum = s_all_sums[wave];
-  // In base and y lane l has outputs 8 (l%16) + (0..7) of rows order[4 i + l/16].
+  // In base and y lane l has outputs 8 (l%8) + (0..7) of rows order[8 i + l/8].
   const int o_begin = (blockIdx.x - s.first_up) * s.up_outputs;
   const int o_end = min(s.rows, o_begin + s.up_outputs);
+  const int o_lane = half * kOut + (lane & 7) * 8;
   int rows[4];
   v4u bases[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) rows[i] = order[4 * i + g];
+  for (int i = 0; i < 4; ++i) rows[i] = idle ? -1 : order[8 * i + (lane >> 3)];
   auto request = [&](int o0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (o0 + m * 8 < s.rows && rows[i] >= 0)
+      if (o0 + o_lane < s.rows && rows[i] >= 0)
         bases[i] = __builtin_nontemporal_load(
             reinterpret_cast<const v4u*>(static_cast<const __half*>(s.base) +
-                                         (int64_t)rows[i] * s.rows + o0 + m * 8));
+                                         (int64_t)rows[i] * s.rows + o0 + o_lane));
   };
   request(o_begin);
   if (a >= 0) {
-    // four lanes a row, four ranks at a time
+    // a wave has 16 of its tile's rows: four lanes a row, four ranks at a time
     constexpr int kAtOnce = 8;
-    const int part = lane & 3, t = max(order[lane >> 2], 0);
-    uint32_t* pair = s_pair + (lane >> 2) * stride;
+    const int row = half * 16 + (lane >> 2), part = lane & 3, t = max(order[row], 0);
+    uint32_t* pair = s_pair + row * stride;
     float top = 0.f;
 #pragma unroll 2
     for (int j = part * 4; j < ranks; j += 16) {
@@ -565,14 +571,10 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
       }
       *at = v;
     }
-    if (part == 0) s_factor[lane >> 2] = ldexpf(p.scales[a], e - 10);
+    if (part == 0) s_factor[row] = ldexpf(p.scales[a], e - 10);
   }
-  // a wave's own LDS accesses stay in order
-  auto settle = [] {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  };
-  settle();
+  __syncthreads();
+  if (idle) return;
   // This lane's 8 ranks of a block, and which parts: all high ones, or with BLOCK 16
   // the low ones for the upper half of the lanes.
   const int at = BLOCK == 16 ? (g & 1) * 8 : g * 8;
@@ -580,36 +582,49 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
   const uint32_t select = BLOCK == 16 && g >= 2 ? low : high;
   const __half* B = s.B + (int64_t)max(a, 0) * s.rows * s.rank + at;
   __half* y = static_cast<__half*>(s.y);
+  // a wave's own LDS accesses stay in order
+  auto settle = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
   for (int o0 = o_begin; o0 < o_end; o0 += kUpStep) {
     if (a >= 0) {
-      floatx4 acc[kUpStep / 16];
+      floatx4 acc[2][kOut / 16];
 #pragma unroll
-      for (int u = 0; u < kUpStep / 16; ++u) acc[u] = floatx4{0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int u = 0; u < kOut / 16; ++u) acc[r][u] = floatx4{0.f, 0.f, 0.f, 0.f};
       for (int j = 0; j < ranks; j += BLOCK) {
-        v4u bv[kUpStep / 16];
+        v4u bv[kOut / 16];
 #pragma unroll
-        for (int u = 0; u < kUpStep / 16; ++u) {
-          const int o = min(o0 + 16 * u + m, s.rows - 1);
+        for (int u = 0; u < kOut / 16; ++u) {
+          const int o = min(o0 + half * kOut + 16 * u + m, s.rows - 1);
           bv[u] = v4u{0, 0, 0, 0};
           if (j + at < s.rank)
             bv[u] = *reinterpret_cast<const v4u*>(B + (int64_t)o * s.rank + j);
         }
-        const uint32_t* pair = &s_pair[m * stride + j + at];
-        const v4u p0 = *reinterpret_cast<const v4u*>(pair);
-        const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
-        const v4u hv = parts(p0, p1, select);
 #pragma unroll
-        for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], hv, acc[u]);
-        if constexpr (BLOCK == 32) {
-          const v4u lv = parts(p0, p1, low);
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t* pair = &s_pair[(16 * r + m) * stride + j + at];
+          const v4u p0 = *reinterpret_cast<const v4u*>(pair);
+          const v4u p1 = *reinterpret_cast<const v4u*>(pair + 4);
+          const v4u hv = parts(p0, p1, select);
 #pragma unroll
-          for (int u = 0; u < kUpStep / 16; ++u) acc[u] = mfma(bv[u], lv, acc[u]);
+          for (int u = 0; u < kOut / 16; ++u) acc[r][u] = mfma(bv[u], hv, acc[r][u]);
+          if constexpr (BLOCK == 32) {
+            const v4u lv = parts(p0, p1, low);
+#pragma unroll
+            for (int u = 0; u < kOut / 16; ++u) acc[r][u] = mfma(bv[u], lv, acc[r][u]);
+          }
         }
       }
-      const float f = s_factor[m];
 #pragma unroll
-      for (int u = 0; u < kUpStep / 16; ++u)
-        *reinterpret_cast<floatx4*>(&s_sum[m][16 * u + 4 * g]) = f * acc[u];
+      for (int r = 0; r < 2; ++r) {
+        const float f = s_factor[16 * r + m];
+#pragma unroll
+        for (int u = 0; u < kOut / 16; ++u)
+          *reinterpret_cast<floatx4*>(&s_sum[16 * r + m][16 * u + 4 * g]) = f * acc[r][u];
+      }
     }
     settle();
     v4u out[4];
@@ -617,7 +632,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
     for (int i = 0; i < 4; ++i) {
       out[i] = bases[i];
       if (a < 0) continue;
-      const float* sum = &s_sum[4 * i + g][m * 8];
+      const float* sum = &s_sum[8 * i + (lane >> 3)][(lane & 7) * 8];
       const floatx4 lo = *reinterpret_cast<const floatx4*>(sum);
       const floatx4 hi = *reinterpret_cast<const floatx4*>(sum + 4);
       const __half* b = reinterpret_cast<const __half*>(&bases[i]);
@@ -630,8 +645,8 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
     if (o0 + kUpStep < o_end) request(o0 + kUpStep);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (o0 + m * 8 < s.rows && rows[i] >= 0)
-        *reinterpret_cast<v4u*>(y + (int64_t)rows[i] * s.rows + o0 + m * 8) = out[i];
+      if (o0 + o_lane < s.rows && rows[i] >= 0)
+        *reinterpret_cast<v4u*>(y + (int64_t)rows[i] * s.rows + o0 + o_lane) = out[i];
   }
 }
 
