@@ -205,7 +205,8 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  *   A      device fp16 [adapters][rank][cols], contiguous
  *   B      device fp16 [adapters][rows][rank], contiguous
  *   base   device [tokens][rows] of y_dtype, contiguous
- *   y      as base; may be base (only rows with an adapter are then written)
+ *   y      as base; may be base (only rows with an adapter are then written);
+ *          otherwise no y overlaps another array of the call
  *   adapter  device int32 [tokens], in any order; a value outside
  *          [0, adapters) means none: y_i[t] = base_i[t]
  *   scales device fp32 [adapters]

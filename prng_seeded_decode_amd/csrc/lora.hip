@@ -37,9 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunk = 8 * kThreads;  // columns of a workgroup of the row kernels
-constexpr int kTileRows = 32;    // rows of a tile, of one adapter
-constexpr int kDownRanks = 64;   // ranks at most of a down workgroup
-constexpr int kDownStep = 256;   // columns staged at once
+constexpr int kTileRows = 32;         // rows of a tile, of one adapter
+constexpr int kDownRanks = 64;        // ranks at most of a down workgroup
+constexpr int kDownStep = 256;        // columns staged at once
 constexpr int kUpRows = 2 * kTileRows;  // rows of an up workgroup, two waves per tile
 constexpr int kUpStep = 128;            // outputs of its step
 static_assert(kWaves == 4, "the tile kernels share tiles out to four waves");
@@ -54,13 +54,13 @@ struct Site {
   const __half* B;
   const void* base;
   void* y;
-  float* h;       // [chunks][tokens][rank]
+  float* h;        // [chunks][tokens][rank]
   int rows, cols, rank;
   int chunks;
-  int chunk_cols; // columns of a chunk
-  int up_outputs; // outputs of an up workgroup
-  int wide;       // 16-byte accesses fit
-  int first_down; // first workgroup (x dimension) of this site in the two launches
+  int chunk_cols;  // columns of a chunk
+  int up_outputs;  // outputs of an up workgroup
+  int wide;        // 16-byte accesses fit
+  int first_down;  // first workgroup (x dimension) of this site in the two launches
   int first_up;
 };
 
@@ -80,12 +80,6 @@ __device__ const Site& site_of(const LoraArgs& p, bool up, int block) {
   for (int k = 1; k < p.n; ++k)
     if (block >= (up ? p.s[k].first_up : p.s[k].first_down)) i = k;
   return p.s[i];
-}
-
-__device__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
 }
 
 template <typename T>
