@@ -15,6 +15,7 @@ MAX_REQUESTS = 4096
 MAX_RANK = 256
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_INT32_MAX = 2 ** 31 - 1  # a ctypes field would take a larger number modulo 2^32
 
 
 class _PlanArgs(ctypes.Structure):
@@ -144,6 +145,8 @@ class CachePlanCall(_Call):
         n, tokens = lens.numel(), rows.numel()
         if table.shape[0] != n:
             raise ValueError("table must have a row for each request")
+        if not 0 < page_size <= _INT32_MAX:
+            raise ValueError("page_size must be positive and fit 32 bits")
         at, max_pages, stride = _table(table)
         args = _PlanArgs(
             _ints("lens", lens, n), _ints("fresh", fresh, n), at,
@@ -221,12 +224,15 @@ class CacheAttendCall(_Call):
         if rows is None and table.shape[0] < n:
             raise ValueError("without rows, table must have a row for each query")
         code = _dtype_code(q)
-        room = max_pages * cache.page_size
+        room = min(max_pages * cache.page_size, _INT32_MAX)
+        if max_len is not None and max_len < 0:
+            raise ValueError("max_len must not be negative")
         args = _AttendArgs(
             q.data_ptr(), out.data_ptr(), at, None if rows is None else _ints("rows", rows, n),
             _ints("lens", lens, n), cache,
             _heads("q", q, n, heads, dim, q.dtype), _heads("out", out, n, heads, dim, q.dtype),
-            stride, n, table.shape[0], heads, max_pages, room if max_len is None else min(max_len, room), code,
+            stride, n, table.shape[0], heads, max_pages,
+            room if max_len is None else min(max_len, room), code,
             dim ** -0.5 if scale is None else scale)
         self._set("seedlm_cache_attend", lib().seedlm_cache_attend, (ctypes.byref(args),), keep,
                   device, stream)

@@ -277,3 +277,21 @@ def test_attend_of_several_queries_per_request():
         ref, tol = R.attend(q[i].double().cpu().numpy(), x["keys"][row][:n], x["values"][row][:n],
                             np.float64(np.float32(128 ** -0.5)), True)
         assert np.all(np.abs(got[i] - ref) <= tol), i
+
+
+def test_attend_with_a_table_that_holds_more_than_32_bits_of_tokens():
+    # 2^21 pages of 2048 tokens: refused by its own bound, taken with the caller's
+    import torch
+
+    import prng_seeded_decode_amd as S
+
+    x = make([15], [90], 4, 2, 64, 2048, True)
+    wide = torch.full((1, 2 ** 21), -1, dtype=torch.int32, device="cuda")
+    wide[:, 0] = x["dtable"][:, 0]
+    y = dict(x, dtable=wide)
+    with pytest.raises(S.SeedLMError) as refused:
+        run(y)
+    assert refused.value.status == S.E_UNSUPPORTED
+    with pytest.raises(ValueError):
+        run(y, max_len=-1)
+    check(x, run(y, max_len=100))
