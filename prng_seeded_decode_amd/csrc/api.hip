@@ -330,7 +330,10 @@ int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out) {
   size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
   if (e && want < 2 * e->bytes) want = 2 * e->bytes;
   void* p = nullptr;
-  if (hipMalloc(&p, want) != hipSuccess) return SEEDLM_E_NOMEM;
+  if (hipMalloc(&p, want) != hipSuccess) {
+    (void)hipGetLastError();  // it is reported here, not by the next launch
+    return SEEDLM_E_NOMEM;
+  }
   try {
     if (e) {
       g_retired.push_back(*e);

@@ -731,7 +731,7 @@ int up_outputs_of(const seedlm_lora_site& s, int n, int64_t tokens, int chunks) 
 
 // Tiles at most: each adapter, and the rows without one, may leave one part-filled.
 int64_t tiles_most(int64_t tokens, int adapters) {
-  const int64_t some = tokens < adapters + 1 ? tokens : adapters + 1;
+  const int64_t buckets = (int64_t)adapters + 1, some = tokens < buckets ? tokens : buckets;
   return (tokens + kTileRows - 1) / kTileRows + some;
 }
 // Scratch of the tiles: their number, adapters and rows, and the rows' places.
