@@ -146,7 +146,12 @@ SEEDLM_API int seedlm_pack(const void* seeds, const int8_t* coeffs,
  * workgroups write fp32 partials into scratch that the library keeps per
  * (device, stream): calls on one stream share it in stream order, and calls on
  * different streams -- with the same handle or not -- use different scratch, so
- * they may overlap.  The first call on a stream, or one that needs more
+ * they may overlap.  Several host threads may call on one stream: a call that uses
+ * the scratch makes all its launches before another such call on that stream makes
+ * any.  Streams are told apart by handle alone, so hipStreamPerThread may be used by
+ * one thread only.  A graph captured from a call uses the scratch of the stream that
+ * it was captured on, wherever it is replayed: a replay must not overlap a call on
+ * that stream, nor a replay of another graph captured there.  The first call on a stream, or one that needs more
  * scratch than any earlier call on that stream, allocates it (hipMalloc: not
  * inside graph capture, so run one call on a stream before capturing it);
  * outgrown scratch stays allocated, so graphs captured from earlier calls stay

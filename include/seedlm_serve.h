@@ -10,7 +10,9 @@
  * read during the call only.  No call synchronises or copies to the host, so
  * each can be captured into a HIP graph; a call that uses scratch follows the
  * scratch rules of seedlm_gemv (per device and stream, allocated by the first
- * call that needs it, freed by seedlm_scratch_release).
+ * call that needs it, freed by seedlm_scratch_release; a replay of a captured
+ * graph must not overlap a call on the stream that it was captured on, nor a
+ * replay of another graph captured there).
  *
  * The paged cache.  Keys and values live in two fp16 pools of `pages` pages of
  * `page_size` tokens.  Element (page, token, head, d) of either pool sits at

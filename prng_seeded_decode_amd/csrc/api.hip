@@ -52,15 +52,21 @@ bool on_handle_device(const seedlm_matrix* h) {
 // buffer that is too small is replaced by one at least twice its size; the old
 // one stays allocated (retired) until seedlm_scratch_release, so launches still
 // in flight, and graphs captured from earlier calls, keep valid memory.
+// Entries, newest first, stay until the process ends.  An entry's mutex guards its
+// buffers, and is held while a call that uses them makes its launches.
 struct StreamScratch {
   int device;
   hipStream_t stream;
-  void* ptr;
-  size_t bytes;
+  StreamScratch* next;
+  std::mutex mu;
+  void* ptr = nullptr;
+  size_t bytes = 0;
+  std::vector<void*> retired;
+
+  StreamScratch(int d, hipStream_t s, StreamScratch* n) : device(d), stream(s), next(n) {}
 };
-std::mutex g_scratch_mu;
-std::vector<StreamScratch> g_scratch;
-std::vector<StreamScratch> g_retired;
+std::mutex g_scratch_mu;  // of the list's head
+StreamScratch* g_scratch = nullptr;
 
 // ---- timing events of the main kernels (measurement only) ----
 struct TimingEvents {
@@ -259,10 +265,11 @@ int run_gemv(const seedlm_handle* hs, const void* const* x, void* const* y, int 
   if (st != SEEDLM_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* base = nullptr;
+  ScratchHold hold;
   if (total > 0) {
     void* p = nullptr;
     if (src == kStreamScratch) {
-      st = stream_scratch(hs[0]->device, s, (size_t)total * sizeof(float), &p);
+      st = hold.take(hs[0]->device, s, (size_t)total * sizeof(float), &p);
     } else {
       if ((size_t)total * sizeof(float) > kStaticScratchBytes) return SEEDLM_E_SCRATCH_LIMIT;
       st = static_scratch(hs[0]->device, &p);
@@ -318,35 +325,36 @@ int run_gemv(const seedlm_handle* hs, const void* const* x, void* const* y, int 
 
 }  // namespace
 
-int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out) {
-  std::lock_guard<std::mutex> lock(g_scratch_mu);
-  StreamScratch* e = nullptr;
-  for (StreamScratch& c : g_scratch)
-    if (c.device == dev && c.stream == s) e = &c;
-  if (e && e->bytes >= bytes) {
-    *out = e->ptr;
-    return SEEDLM_OK;
-  }
-  size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
-  if (e && want < 2 * e->bytes) want = 2 * e->bytes;
-  void* p = nullptr;
-  if (hipMalloc(&p, want) != hipSuccess) {
-    (void)hipGetLastError();  // it is reported here, not by the next launch
-    return SEEDLM_E_NOMEM;
-  }
-  try {
-    if (e) {
-      g_retired.push_back(*e);
-      e->ptr = p;
-      e->bytes = want;
-    } else {
-      g_scratch.push_back(StreamScratch{dev, s, p, want});
+int ScratchHold::take(int dev, hipStream_t s, size_t bytes, void** out) {
+  StreamScratch* e;
+  {
+    std::lock_guard<std::mutex> lock(g_scratch_mu);
+    for (e = g_scratch; e && (e->device != dev || e->stream != s);) e = e->next;
+    if (!e) {
+      e = new (std::nothrow) StreamScratch(dev, s, g_scratch);
+      if (!e) return SEEDLM_E_NOMEM;
+      g_scratch = e;
     }
-  } catch (const std::bad_alloc&) {
-    (void)hipFree(p);
-    return SEEDLM_E_NOMEM;
   }
-  *out = p;
+  lock_ = std::unique_lock<std::mutex>(e->mu);
+  if (e->bytes < bytes) {
+    size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
+    if (want < 2 * e->bytes) want = 2 * e->bytes;
+    void* p = nullptr;
+    if (hipMalloc(&p, want) != hipSuccess) {
+      (void)hipGetLastError();  // it is reported here, not by the next launch
+      return SEEDLM_E_NOMEM;
+    }
+    try {
+      if (e->ptr) e->retired.push_back(e->ptr);
+    } catch (const std::bad_alloc&) {
+      (void)hipFree(p);
+      return SEEDLM_E_NOMEM;
+    }
+    e->ptr = p;
+    e->bytes = want;
+  }
+  *out = e->ptr;
   return SEEDLM_OK;
 }
 
@@ -444,18 +452,27 @@ int seedlm_bench_time_next_call(void* start_event, void* stop_event) {
 }
 
 int seedlm_scratch_release(void) {
-  std::lock_guard<std::mutex> lock(g_scratch_mu);
   int cur = 0;
   if (hipGetDevice(&cur) != hipSuccess) return SEEDLM_E_DEVICE;
   int rc = SEEDLM_OK;
-  for (std::vector<StreamScratch>* list : {&g_scratch, &g_retired}) {
-    for (StreamScratch& e : *list) {
-      if (!e.ptr) continue;
-      if (hipSetDevice(e.device) != hipSuccess || hipDeviceSynchronize() != hipSuccess ||
-          hipFree(e.ptr) != hipSuccess)
-        rc = SEEDLM_E_DEVICE;
+  StreamScratch* e;
+  {
+    std::lock_guard<std::mutex> lock(g_scratch_mu);
+    e = g_scratch;
+  }
+  for (; e; e = e->next) {
+    std::lock_guard<std::mutex> lock(e->mu);  // a call that holds it has made its launches
+    if (!e->ptr) continue;
+    if (hipSetDevice(e->device) != hipSuccess || hipDeviceSynchronize() != hipSuccess) {
+      rc = SEEDLM_E_DEVICE;
+      continue;  // kernels may still use it
     }
-    list->clear();
+    for (void* p : e->retired)
+      if (hipFree(p) != hipSuccess) rc = SEEDLM_E_DEVICE;
+    if (hipFree(e->ptr) != hipSuccess) rc = SEEDLM_E_DEVICE;
+    e->retired.clear();
+    e->ptr = nullptr;
+    e->bytes = 0;
   }
   if (hipSetDevice(cur) != hipSuccess) rc = SEEDLM_E_DEVICE;
   return rc;
@@ -488,9 +505,10 @@ int seedlm_gemm(seedlm_handle h, const void* X, void* Y, int64_t ntok, int x_dty
   if (st != SEEDLM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   void* part = nullptr;
+  ScratchHold hold;
   const size_t bytes = gemm_scratch_bytes(h, ntok);
   if (bytes > 0) {
-    st = stream_scratch(h->device, s, bytes, &part);
+    st = hold.take(h->device, s, bytes, &part);
     if (st != SEEDLM_OK) return st;
   }
   return launch_gemm(h, X, Y, ntok, static_cast<float*>(part), s);

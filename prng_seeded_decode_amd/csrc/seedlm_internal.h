@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/seedlm.h"
 #include "../../include/seedlm_bench.h"
 #include "../../include/seedlm_serve.h"
@@ -177,9 +179,19 @@ size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, 
 int launch_lora(const seedlm_lora_site* sites, int n, const int32_t* adapter, const float* scales,
                 int64_t tokens, int adapters, int xdt, int ydt, float* scratch, hipStream_t s);
 
-// The library's scratch of a stream of device `dev`, at least `bytes` large
-// (calls on one stream share it in stream order).
-int stream_scratch(int dev, hipStream_t s, size_t bytes, void** out);
+// A stream's scratch for the length of one call.  take() gives the library's
+// scratch of a stream of device `dev`, at least `bytes` large (calls on one
+// stream share it in stream order).  From then until the object goes, other
+// host threads wait in take() for the same stream: a call hands partial results
+// from launch to launch, and another call's launch between them would use the
+// same memory.  Keep it until the call's last launch.
+class ScratchHold {
+ public:
+  int take(int dev, hipStream_t s, size_t bytes, void** out);
+
+ private:
+  std::unique_lock<std::mutex> lock_;
+};
 
 // Number of compute units of the current device (cached per device).
 int device_cu_count();

@@ -15,13 +15,13 @@ bool overlap(const int32_t* p, int64_t n, const int32_t* q, int64_t m) {
   return a < b + (uintptr_t)m * 4 && b < a + (uintptr_t)n * 4;
 }
 
-// Scratch of `bytes` bytes on `s` (NULL for none).
-int scratch_for(hipStream_t s, size_t bytes, void** out) {
+// Scratch of `bytes` bytes on `s` (NULL for none), held for the call's launches.
+int scratch_for(ScratchHold* hold, hipStream_t s, size_t bytes, void** out) {
   *out = nullptr;
   if (bytes == 0) return SEEDLM_OK;
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return SEEDLM_E_DEVICE;
-  return stream_scratch(dev, s, bytes, out);
+  return hold->take(dev, s, bytes, out);
 }
 
 int check_plan(const seedlm_cache_plan_args* a) {
@@ -149,8 +149,9 @@ int seedlm_cache_plan(const seedlm_cache_plan_args* args, void* stream) {
   int st = check_plan(args);
   if (st != SEEDLM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  ScratchHold hold;
   void* scratch = nullptr;
-  st = scratch_for(s, cache_plan_scratch_bytes(*args), &scratch);
+  st = scratch_for(&hold, s, cache_plan_scratch_bytes(*args), &scratch);
   if (st != SEEDLM_OK) return st;
   return launch_cache_plan(*args, static_cast<int32_t*>(scratch), s);
 }
@@ -165,8 +166,9 @@ int seedlm_cache_attend(const seedlm_cache_attend_args* args, void* stream) {
   int st = check_attend(args);
   if (st != SEEDLM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  ScratchHold hold;
   void* scratch = nullptr;
-  st = scratch_for(s, cache_attend_scratch_bytes(*args), &scratch);
+  st = scratch_for(&hold, s, cache_attend_scratch_bytes(*args), &scratch);
   if (st != SEEDLM_OK) return st;
   return launch_cache_attend(*args, scratch, s);
 }
@@ -196,8 +198,10 @@ int seedlm_lora_many(const seedlm_lora_site* sites, int n, const int32_t* adapte
       return SEEDLM_E_INVALID;
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  ScratchHold hold;
   void* scratch = nullptr;
-  st = scratch_for(s, lora_scratch_bytes(sites, n, tokens, adapters, x_dtype, y_dtype), &scratch);
+  st = scratch_for(&hold, s, lora_scratch_bytes(sites, n, tokens, adapters, x_dtype, y_dtype),
+                   &scratch);
   if (st != SEEDLM_OK) return st;
   return launch_lora(sites, n, adapter, scales, tokens, adapters, x_dtype, y_dtype,
                      static_cast<float*>(scratch), s);
