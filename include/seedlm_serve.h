@@ -216,7 +216,8 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  * sharing their launches: one for few rows with a small A, two, or three for
  * many rows.  x_dtype and y_dtype are SEEDLM_F32 or SEEDLM_F16.
  * A row's result depends on its own adapter alone: NaN or infinities in other
- * adapters do not reach it.  A x is held in fp32; the sum is rounded once.
+ * adapters do not reach it.  Infinities in its own give the infinity or NaN that
+ * the formula does, whatever the number of rows.  A x is held in fp32; the sum is rounded once.
  * Calls with fp16 x and y and many rows run on the matrix cores, A x entering
  * the second product as the sum of two fp16 numbers (22 bits).
  * Scratch: seedlm_lora_scratch_bytes, on the stream.  tokens = 0 and n = 0 are

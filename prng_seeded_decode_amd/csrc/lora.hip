@@ -19,7 +19,8 @@
 //   down  a tile and up to 64 ranks per workgroup, x and A staged through LDS
 //   up    a tile and 64 outputs per wave and step; the sums turn over in LDS.  h
 //         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
-//         largest |h|); up to rank 16 the 16 high and 16 low parts fill the 32
+//         largest finite |h|), infinities in hi alone and against the high part alone
+//         of B's, so that they give what the formula does; up to rank 16 the 16 high and 16 low parts fill the 32
 //         products of one MFMA against the same 16 elements of B twice.
 // The bytes of x, base and y bound these.
 //
@@ -481,6 +482,16 @@ __device__ v4u parts(v4u p0, v4u p1, uint32_t select) {
   return v4u{pick(p0[1], p0[0]), pick(p0[3], p0[2]), pick(p1[1], p1[0]), pick(p1[3], p1[2])};
 }
 
+// fp16 values with +-65504 for infinities and NaN (as integers fp16 values of one sign
+// are in order; negative ones lie below the positive as int16, above them as uint16).
+typedef int16_t short8 __attribute__((ext_vector_type(8)));
+typedef uint16_t ushort8 __attribute__((ext_vector_type(8)));
+__device__ v4u limit(v4u v) {
+  const short8 p = __builtin_elementwise_min(__builtin_bit_cast(short8, v), (short8)(int16_t)0x7BFF);
+  return __builtin_bit_cast(
+      v4u, __builtin_elementwise_min(__builtin_bit_cast(ushort8, p), (ushort8)(uint16_t)0xFBFF));
+}
+
 // y of two tiles' rows and s.up_outputs outputs; of a step, a wave has its tile's rows
 // and 64 outputs, so that B is loaded once for 32 rows (the vector cache's accesses
 // bound higher ranks).  BLOCK: ranks of a pass, 16 (for at most 16: high and low parts
@@ -529,7 +540,8 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
     constexpr int kAtOnce = 8;
     const int row = half * 16 + (lane >> 2), part = lane & 3, t = max(order[row], 0);
     uint32_t* pair = s_pair + row * stride;
-    float top = 0.f;
+    float top = 0.f;          // the row's largest |h|
+    uint32_t low = ~0u;       // and the bits of its smallest one but zero, times 2, less 1
 #pragma unroll 2
     for (int j = part * 4; j < ranks; j += 16) {
       floatx4 sum = {0.f, 0.f, 0.f, 0.f};
@@ -546,21 +558,47 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
         for (int c = 0; c < kAtOnce; ++c) sum += v[c];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(sum[i]));
+      for (int i = 0; i < 4; ++i) {
+        top = fmaxf(top, fabsf(sum[i]));
+        low = min(low, (__float_as_uint(sum[i]) << 1) - 1u);
+      }
       *reinterpret_cast<floatx4*>(&pair[j]) = sum;
     }
     top = fmaxf(top, __shfl_xor(top, 1));
     top = fmaxf(top, __shfl_xor(top, 2));
-    // the row's largest value into [2^9, 2^10): the low parts keep all bits
-    int e = 10;
-    if (top > 0.f && top < INFINITY) (void)frexpf(top, &e);
+    // the row's largest finite value into [2^9, 2^10): the low parts keep all bits
+    auto exponent = [&] {
+      top = fmaxf(top, __shfl_xor(top, 1));
+      top = fmaxf(top, __shfl_xor(top, 2));
+      int e = 10;
+      if (top > 0.f && top < INFINITY) (void)frexpf(top, &e);
+      return e;
+    };
+    int e = exponent();
+    // rows with an infinity, or with a value that is too small for fp16 beside the largest
+    const float least = __uint_as_float((low + 1u) >> 1);
+    const bool odd = __any(top == INFINITY || (least > 0.f && ldexpf(least, 10 - e) < 0x1p-24f));
+    if (odd) {
+      top = 0.f;
+      for (int j = part * 4; j < ranks; j += 16)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float h = fabsf(__uint_as_float(pair[j + i]));
+          top = fmaxf(top, h < INFINITY ? h : 0.f);
+        }
+      e = exponent();
+    }
     for (int j = part * 4; j < ranks; j += 16) {
       v4u* at = reinterpret_cast<v4u*>(&pair[j]);
       v4u v = *at;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float f = ldexpf(__uint_as_float(v[i]), 10 - e);
-        const _Float16 hi = (_Float16)f, lo = (_Float16)(f - (float)hi);
+        const float h = __uint_as_float(v[i]), f = ldexpf(h, 10 - e);
+        _Float16 hi = (_Float16)f, lo = (_Float16)(f - (float)hi);
+        if (odd) {  // the formula's infinity or NaN comes from hi, which is 0 for 0 alone
+          if (hi == (_Float16)0.f && h != 0.f) hi = (_Float16)copysignf(0x1p-14f, h);
+          lo = (_Float16)(fabsf(f) < INFINITY ? f - (float)hi : 0.f);
+        }
         v[i] = __builtin_bit_cast(uint16_t, hi) | (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
       }
       *at = v;
@@ -597,6 +635,14 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
           if (j + at < s.rank)
             bv[u] = *reinterpret_cast<const v4u*>(B + (int64_t)o * s.rank + j);
         }
+        // B for the low parts is finite: an infinity, which the high part shows, times a
+        // low part that is zero or of the other sign would be NaN
+        v4u bl[kOut / 16];
+#pragma unroll
+        for (int u = 0; u < kOut / 16; ++u) {
+          bl[u] = limit(bv[u]);
+          if constexpr (BLOCK == 16) bv[u] = select == low ? bl[u] : bv[u];
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t* pair = &s_pair[(16 * r + m) * stride + j + at];
@@ -608,7 +654,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_tile_kernel(const LoraArgs p
           if constexpr (BLOCK == 32) {
             const v4u lv = parts(p0, p1, low);
 #pragma unroll
-            for (int u = 0; u < kOut / 16; ++u) acc[r][u] = mfma(bv[u], lv, acc[r][u]);
+            for (int u = 0; u < kOut / 16; ++u) acc[r][u] = mfma(bl[u], lv, acc[r][u]);
           }
         }
       }
