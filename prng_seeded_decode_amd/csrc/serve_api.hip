@@ -112,10 +112,11 @@ int check_attend(const seedlm_cache_attend_args* a) {
     return SEEDLM_E_UNSUPPORTED;
   // Token offsets are 32-bit counts of 8 elements.
   constexpr int64_t kMost = (int64_t)1 << 35;
+  // (each stride's own bound first, so that the products fit 64 bits)
   if (c.page_stride >= kMost / c.pages || c.token_stride >= kMost / c.page_size ||
+      c.head_stride >= kMost / c.kv_heads ||
       c.page_stride * (c.pages - 1) + c.token_stride * (c.page_size - 1) >=
-          kMost - 8 - c.head_stride * (c.kv_heads - 1) - c.head_dim ||
-      c.head_stride >= kMost / c.kv_heads)
+          kMost - 8 - c.head_stride * (c.kv_heads - 1) - c.head_dim)
     return SEEDLM_E_UNSUPPORTED;
   const int64_t room = (int64_t)a->max_pages * c.page_size;
   // Token numbers, and the sums of 128-token units over the requests, are 32-bit.
