@@ -189,8 +189,11 @@ def _stream_ptr(stream):
         import torch
 
         # torch.cuda.current_stream().cuda_stream without the Stream object, whose
-        # making costs 2.8 us a call, as much as a launch
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        # making costs 2.8 us a call, as much as a launch; the query is private to torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(raw(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
