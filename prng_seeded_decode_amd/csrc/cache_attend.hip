@@ -547,13 +547,17 @@ Scratch scratch_of(const seedlm_cache_attend_args& a) {
 }
 
 // Whether keys and values pass the caches: a call that may read more than the 256
-// MB of the memory-side cache finds nothing of it there the next time.  One request
-// of 131071 tokens 101 -> 97 us, 64 of up to 16384 376 -> 369, 16 of 16384 in 256
-// dimensions 347 -> 323; 64 dimensions gain nothing (442 and 456).  A cache that fits
-// would lose: 16 requests of 2048, read again and again, 29 -> 33 us.
+// MB of the memory-side cache finds nothing of it there the next time.  Where rows are
+// given, queries may share a request's tokens, which the caches then serve to all but
+// the first.  Time of a call, passing the caches against not, 8 cache heads, fp16: one
+// request of 131071 tokens in 128 dimensions 102 and 105 us, 64 of up to 16384 (32 heads)
+// 357 and 361, 16 of 16384 in 256 dimensions 325 and 338; 64 dimensions gain nothing (442
+// and 456).  A cache that fits would lose: 16 requests of 2048 in 128 dimensions, read
+// again and again, 33 and 29.  So would prompts: 2048 queries of one request 1025 and
+// 947, 512 queries behind 8192 cached tokens (64 heads) 2323 and 1226.
 bool streams(const seedlm_cache_attend_args& a) {
   const int64_t most = (int64_t)a.queries * cap_of(a) * a.cache.kv_heads * a.cache.head_dim * 4;
-  return a.cache.head_dim > 64 && most > (int64_t)256 << 20;
+  return !a.rows && a.cache.head_dim > 64 && most > (int64_t)256 << 20;
 }
 
 template <int D, bool WIDE>

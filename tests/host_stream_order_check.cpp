@@ -11,6 +11,9 @@
 //       calls on two streams: neither waits for the other
 //   host_stream_order_check <libseedlm.so> release
 //       seedlm_scratch_release beside a call: no launch gets freed memory
+//   host_stream_order_check <libseedlm.so> loads
+//       attention whose queries may share their tokens runs the kernel whose loads
+//       stay in the caches, whatever the bound on its lengths
 //
 // Exit status 0 when the check holds.
 #include <dlfcn.h>
@@ -36,6 +39,7 @@ namespace {
 struct Launch {
   hipStream_t stream;
   int call;
+  const void* kernel;
 };
 std::mutex g_mu;
 std::condition_variable g_changed;
@@ -58,10 +62,10 @@ void fail(const char* what) {
   ++g_failures;
 }
 
-hipError_t launch(hipStream_t stream, void** args) {
+hipError_t launch(const void* kernel, hipStream_t stream, void** args) {
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    g_launches.push_back({stream, t_call});
+    g_launches.push_back({stream, t_call, kernel});
   }
   ++t_nth;
   g_changed.notify_all();
@@ -91,12 +95,12 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
   *stream = t_config.stream;
   return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void*, dim3, dim3, void** args, size_t, hipStream_t stream) {
-  return launch(stream, args);
+hipError_t hipLaunchKernel(const void* kernel, dim3, dim3, void** args, size_t, hipStream_t stream) {
+  return launch(kernel, stream, args);
 }
-hipError_t hipExtLaunchKernel(const void*, dim3, dim3, void** args, size_t, hipStream_t stream,
+hipError_t hipExtLaunchKernel(const void* kernel, dim3, dim3, void** args, size_t, hipStream_t stream,
                               hipEvent_t, hipEvent_t, int) {
-  return launch(stream, args);
+  return launch(kernel, stream, args);
 }
 hipError_t hipMalloc(void** p, size_t n) {
   *p = aligned_alloc(256, (n + 255) / 256 * 256);
@@ -283,6 +287,30 @@ int release(const Calls& calls, void* lib) {
   return g_failures != 0;
 }
 
+int loads(void* lib) {
+  const auto attend = symbol<decltype(&seedlm_cache_attend)>(lib, "seedlm_cache_attend");
+  int32_t* const i = reinterpret_cast<int32_t*>(4096);
+  auto kernel_of = [&](int queries, const int32_t* rows, int dim, int dtype) {
+    seedlm_cache_attend_args t{};
+    t.q = i, t.out = i, t.table = i, t.lens = i, t.rows = rows;
+    t.cache = {i, i, 100000, 16 * 2 * dim, 2 * dim, dim, 16, 2, dim};
+    t.q_stride = t.out_stride = 4 * dim;
+    t.table_stride = t.max_pages = 512;
+    t.queries = t.table_rows = queries, t.heads = 4, t.max_len = 8192;
+    t.x_dtype = dtype, t.scale = 0.1f;
+    g_launches.clear();
+    if (attend(&t, nullptr) != SEEDLM_OK || g_launches.empty()) fail("attend");
+    return g_launches.empty() ? nullptr : g_launches[0].kernel;
+  };
+  for (int dim : {128, 256})
+    for (int dtype : {SEEDLM_F32, SEEDLM_F16}) {
+      const void* cached = kernel_of(3, nullptr, dim, dtype);  // 25 and 50 MB at most
+      if (kernel_of(64, nullptr, dim, dtype) == cached) fail("64 requests of 8192 tokens are small");
+      if (kernel_of(64, i, dim, dtype) != cached) fail("queries that may share tokens pass the caches");
+    }
+  return g_failures != 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -296,7 +324,7 @@ int main(int argc, char** argv) {
   g_launches.clear();
   const std::string mode = argv[2];
   const int rc = mode == "same" ? same(calls) : mode == "other" ? other(calls)
-               : mode == "release" ? release(calls, lib) : 2;
+               : mode == "release" ? release(calls, lib) : mode == "loads" ? loads(lib) : 2;
   printf("%s: %d failure(s)\n", argv[2], g_failures.load());
   return rc;
 }

@@ -1,5 +1,6 @@
-"""Calls of several host threads on one stream (CPU only): host_stream_order_check.cpp loads the
-built library on top of a stand-in for the HIP runtime and looks at the order of its launches."""
+"""The launches that calls make (CPU only): host_stream_order_check.cpp loads the built library on
+top of a stand-in for the HIP runtime and looks at their order, where several host threads call on
+one stream, and at the kernel that a call's sizes select."""
 import os
 import subprocess
 
@@ -31,3 +32,8 @@ def test_launches_of_calls_from_several_threads(checker, mode):
     r = subprocess.run([checker, _binding.LIB_PATH, mode], capture_output=True, text=True, timeout=100)
     assert r.returncode == 0, r.stdout + r.stderr
     assert f"{mode}: 0 failure(s)" in r.stdout
+
+
+def test_attention_kernel_of_queries_that_may_share_tokens(checker):
+    r = subprocess.run([checker, _binding.LIB_PATH, "loads"], capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "loads: 0 failure(s)" in r.stdout, r.stdout + r.stderr
