@@ -711,11 +711,15 @@ enum Kind { kOne, kRows, kTiles };
 constexpr int64_t kTileTokens = 64;
 constexpr int64_t kTileBytes = 128 << 20;  // A and B, once per row
 // One launch pays while A is small for a workgroup to read whole and the workgroups
-// are at most the compute units (every one reads A).  One launch against two: q, k
-// and v of a 70B layer at rank 16 6.7 and 7.8 us at 16 rows, 9.0 and 12.0 at 64; gate
-// and up of an 8B layer 5.0 and 6.5 at 1, 7.7 and 9.9 at 32 (256 workgroups), 13.8
-// and 13.5 at 64; 512 x 512 3.9 and 5.8 at 1; 8192 x 28672 10.8 and 8.5.
-constexpr int64_t kOneBytes = 256 << 10;  // of one adapter's A
+// are at most the compute units (every one reads A).  Time of a call, one launch against
+// two, by A's bytes at rank 16 and 4096 rows, fp16 (fp32): 8192 columns, 256 KiB, 6.4 us
+// at 1 row; 14336, 448 KiB, 7.4 and 9.2 at 1 row (7.5 and 10.4), 9.0 and 10.6 at 16 (9.0
+// and 12.9), 10.3 and 13.7 at 64; 16384, 512 KiB, 7.9 and 9.2 at 1 (8.1 and 10.5), 9.6
+// and 9.7 at 4, 9.2 and 11.2 at 16, 11.3 and 14.4 at 64; 20480, 640 KiB, 8.9 and 9.4 at
+// 1, 11.7 and 10.5 at 4 (11.7 and 11.7); 24576 9.6 and 9.5 at 1, 12.5 and 11.0 at 4;
+// 8192 x 28672 12.7 and 10.0 at 1.  By the workgroups: gate and up of an 8B layer 7.7 and
+// 9.9 at 32 rows (256 workgroups), 13.8 and 13.5 at 64.
+constexpr int64_t kOneBytes = 512 << 10;  // of one adapter's A
 
 // Outputs of a workgroup of lora_one_kernel: a row per thread, or up to four where
 // there are more workgroups than compute units; *workgroups gets their number.
