@@ -63,9 +63,9 @@ extern "C" {
  *   spans       int32 [T] or NULL: the tokens that each new token attends to,
  *               position + 1, itself among them; 0 where its slot is -1
  *   ok          int32 [n]: 1 or 0
- * A request's step is granted (ok = 1) if its tokens fit its table row and the
- * T entries, and the queue holds its new pages after those of the requests
- * before it: its new pages come from the queue's front into its table row and
+ * A request's step is granted (ok = 1) if its tokens fit its table row, they and
+ * those of all requests before it fit the T entries, and the queue holds its new
+ * pages after those that requests before it asked for: its new pages come from the queue's front into its table row and
  * its length grows.  Otherwise (ok = 0) it gets no pages, its length stays and
  * its tokens' slots are -1.  A finished request has ok = 1 and length 0; its
  * pages join the queue's end (for later calls) and its table row keeps its
@@ -165,10 +165,12 @@ SEEDLM_API int seedlm_cache_append(const seedlm_cache_append_args* args, void* s
  *          lengths themselves, which only the GPU reads)
  *   scale  finite
  * head_dim 64, 128 or 256; heads a multiple of kv_heads, at most 16384; queries
- * at most SEEDLM_MAX_REQUESTS.  A query of no tokens (length 0, no row, or no
+ * at least 1 and at most SEEDLM_MAX_REQUESTS.  A query of no tokens (length 0, no row, or no
  * valid page) gets zeros.  What lies in the cache beyond a query's length, NaN
- * and infinities included, does not reach its output; an infinity among the
- * values that it does attend to makes it NaN.  Products of fp16 keys are exact;
+ * and infinities included, does not reach its output.  An infinity among the
+ * values that it does attend to makes the output elements that it enters infinite
+ * or NaN.  With fp32 queries one among the keys may make a head's output NaN where
+ * the formula gives the token a weight of 0.  Products of fp16 keys are exact;
  * scores, softmax statistics and sums are fp32, and the softmax weights enter
  * the matrix cores as the sum of two fp16 numbers (22 bits), as do fp32 queries.
  * The cache's base addresses are 16-byte aligned and its strides multiples of
@@ -217,9 +219,10 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  * many rows.  x_dtype and y_dtype are SEEDLM_F32 or SEEDLM_F16.
  * A row's result depends on its own adapter alone: NaN or infinities in other
  * adapters do not reach it.  Infinities in its own give the infinity or NaN that
- * the formula does, whatever the number of rows.  A x is held in fp32; the sum is rounded once.
- * Calls with fp16 x and y and many rows run on the matrix cores, A x entering
- * the second product as the sum of two fp16 numbers (22 bits).
+ * the formula does, whatever the number of rows.  A x is held in fp32; the sum is
+ * rounded once.  Calls with fp16 x and y, many rows and ranks and sizes that are
+ * multiples of 8 run on the matrix cores, A x entering the second product as the
+ * sum of two fp16 numbers (22 bits).
  * Scratch: seedlm_lora_scratch_bytes, on the stream.  tokens = 0 and n = 0 are
  * no-ops.
  * Errors: SEEDLM_E_INVALID (null, range, a pointer not aligned to its type),

@@ -12,7 +12,10 @@
 // Shapes or addresses that rule 16-byte accesses out use units of one pair.
 //
 // Measured: 4097 tokens of 32 query and 32 cache heads of 128 dimensions, fp16 (203
-// MB), in 38.4 us, 5.3 TB/s; 16 tokens of 64 and 8 heads in 3.2 us, a launch's time.
+// MB), in 38.4 us, 5.3 TB/s; 16 tokens of 64 and 8 heads in 2.8 us, a launch's time;
+// 2048 tokens of 32 and 8 heads, fp32 (93 MB), in 18.2 us, 5.1 TB/s, and fp16 with 120
+// of the 128 dimensions rotated, so by units of one pair (51 MB), in 24.6 us, 2.1 TB/s:
+// their 2-byte accesses take 16 times the instructions.
 #include <hip/hip_fp16.h>
 
 #include "seedlm_internal.h"

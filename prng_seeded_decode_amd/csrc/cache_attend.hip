@@ -2,9 +2,9 @@
 // (seedlm_cache_attend): out = sum_t softmax_t(scale q . k_t) v_t.  A query is
 // called a request here; rows of the table tell which pages it has.
 //
-// Every key and value is read once, with 4 flops per query head of the group
-// that shares it (4 to 8 flops per byte at 8 query heads), so memory bandwidth
-// bounds the path once there is enough work, and latency below that.
+// A query reads each of its keys and values once, with 4 flops per query head of
+// the group that shares it (4 to 8 flops per byte at 8 query heads), so memory
+// bandwidth bounds the path once there is enough work, and latency below that.
 //
 // Split.  The lengths lie on the GPU, so every workgroup forms the split itself.
 // A request of len tokens is ceil(len / kUnit) units; the units of all requests,
@@ -37,10 +37,13 @@
 // error as the rounding of an fp16 output does.  fp32 queries are split alike,
 // after scaling each row by a power of two.
 //
-// Measured (main launch, then the join; a streaming read reaches 6.2 TB/s): one
-// request of 131071 tokens of 8 cache heads, 128 dimensions, 537 MB, 97 + 4.7 us, 5.5
-// TB/s, reading 541 MB; 64 ragged requests of up to 16384 tokens, 2.15 GB, 371 + 5.8
-// us, 5.8 TB/s; 16 of up to 8192, 269 MB, 51 + 4.6 us.  Matrix cores are busy 5% of the
+// Measured (main launch, then the join; a streaming read reaches 6.2 TB/s), 8 cache
+// heads: one request of 131071 tokens, 128 dimensions, 537 MB, 98 + 4.8 us, 5.5 TB/s,
+// reading 541 MB; 64 ragged requests of up to 16384 tokens, 2.12 GB, 372 + 6.0 us, 5.7
+// TB/s; 16 of up to 8192, 252 MB, 51 + 4.6 us, with fp32 q the same; in 256 dimensions,
+// 505 MB, 88 + 4.8 us, 5.8 TB/s, with fp32 q the same; in 64 dimensions, 126 MB, 32 + 4.9
+// us, 3.9 TB/s; 8 ragged requests of up to 2047 tokens of 32 heads of 64, fp32 q, 51 MB,
+// 13.3 + 4.0 us.  Matrix cores are busy 5% of the
 // time and vector units 13%: what is left is the start of each run (lengths, page
 // numbers, first keys: 7 to 9 us before the reads are at full rate) and its end.
 #include <hip/hip_fp16.h>

@@ -11,7 +11,7 @@
 // requests with w > 0 take one contiguous run of the queue.
 //
 // The path is bound by latency, not bytes (a step of 16 requests moves under a
-// kilobyte and takes 3.8 us, one of 1000 requests and 80,000 token entries 7.7 us for
+// kilobyte and takes 3.8 us, one of 1000 requests and 80,000 token entries 7.9 us for
 // 1.03 MB), so it is one launch: every workgroup forms the prefix sums of all
 // requests again (at most kMaxRequests, 8 per thread, out of L2) and then
 // handles its share of the pages and tokens, each finding its request by
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(256) void copy_plan_kernel(const int32_t* __restric
 }
 
 // Workgroups of a call: a token per thread, since a thread's tokens would wait for
-// one another's bisection and page number (80,000 tokens: 7 us a call, 12 with four
+// one another's bisection and page number (80,000 tokens: 7.3 us a call, 12 with four
 // tokens each), up to two workgroups per compute unit.
 int plan_grid(const seedlm_cache_plan_args& a) {
   const int g = (a.tokens + kThreads - 1) / kThreads;

@@ -19,15 +19,19 @@
 //   down  a tile and up to 64 ranks per workgroup, x and A staged through LDS
 //   up    a tile and 64 outputs per wave and step; the sums turn over in LDS.  h
 //         enters as two fp16 numbers, h 2^-e = hi + lo (22 bits; e from the row's
-//         largest finite |h|), infinities in hi alone and against the high part alone
-//         of B's, so that they give what the formula does; up to rank 16 the 16 high and 16 low parts fill the 32
-//         products of one MFMA against the same 16 elements of B twice.
-// The bytes of x, base and y bound these.
+//         largest finite |h|).  Infinities are in hi alone, and lo meets a finite B
+//         alone, so that they give what the formula does.  Up to rank 16 the 16 high
+//         and 16 low parts fill the 32 products of one MFMA against the same 16
+//         elements of B twice.
+// The bytes of x, base and y bound these.  Many rows of fp32, and ranks that are no
+// multiple of 8, take the row kernels, which read A and B once per row.
 //
-// Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 8.0 us in
-// one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.6, down 10.0,
-// up 55 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call; 1159 rows on
-// q, k and v of the 70B layer at rank 64, sort 4.9, down 19, up 30 us.
+// Measured: 16 requests on q, k and v of a 70B layer at rank 16 (18.7 MB) 8.1 us in
+// one launch; 2049 rows on gate and up of an 8B layer at rank 16, sort 6.7, down 10.4,
+// up 55 us for 235 MB (4.3 TB/s; a large copy reaches 4.8), 70 us a call; at rank 4, by
+// the row kernels, 54 and 310 us; 512 rows of fp32 at rank 16, likewise, 18 and 84 us;
+// 1159 rows on q, k and v of the 70B layer at rank 64 (102 MB), sort 5.1, down 18.9, up
+// 32 us.
 #include <hip/hip_fp16.h>
 
 #include "seedlm_internal.h"

@@ -91,6 +91,18 @@ def test_nan_stays_with_its_own_request_and_head(dim, wide):
 
 
 @pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_an_infinite_value_stays_with_its_own_dimension(dim, f16):
+    x = make([45, dim], [2000, 1500, 90], 4, 2, dim, 16, f16)
+    clean = run_split(x)
+    x["v_cache"][int(x["table"][1, 3]), 6, 0, 9] = float("-inf")
+    got = run_split(x)
+    assert not np.isfinite(got[1, :2, 9]).any()
+    got[1, :2, 9] = clean[1, :2, 9]
+    assert np.array_equal(got, clean)
+
+
+@pytest.mark.parametrize("f16", [True, False])
 def test_pages_outside_the_cache_and_lengths_past_the_table(f16):
     import torch
 
