@@ -1,8 +1,9 @@
 /*
  * seedlm_serve.h -- what a serving step needs around the packed projections of
  * seedlm.h: page tables and slots of a paged key-value cache, rotary positions
- * with the cache write, attention of new tokens over the cache, and low-rank
- * adapters of many requests beside a shared projection.
+ * with the cache write, attention of new tokens over the cache, the last two and
+ * a read-back for a cache quantised to 4 or 8 bits, and low-rank adapters of
+ * many requests beside a shared projection.
  *
  * Conventions are those of seedlm.h: status codes, dtype codes, streams passed
  * as void*, device pointers of the current device, asynchronous launches, no
@@ -22,6 +23,9 @@
  * token p % page_size of page table[request][p / page_size]; its slot is
  * page * page_size + p % page_size.  A page number outside [0, pages) holds no
  * tokens: nothing is read or written through it.
+ *
+ * The quantised cache has the same pages, tables and slots, and in the place of
+ * fp16 elements codes of 4 or 8 bits with fp16 pairs (seedlm_qcache_t).
  */
 #ifndef SEEDLM_SERVE_H
 #define SEEDLM_SERVE_H
@@ -32,7 +36,7 @@
 extern "C" {
 #endif
 
-/* Most requests of one seedlm_cache_plan call and queries of a seedlm_cache_attend. */
+/* Most requests of one seedlm_cache_plan call and queries of an attention call. */
 #define SEEDLM_MAX_REQUESTS 4096
 /* Largest adapter rank. */
 #define SEEDLM_MAX_RANK 256
@@ -199,6 +203,131 @@ SEEDLM_API int seedlm_cache_attend(const seedlm_cache_attend_args* args, void* s
  * uses for these arguments on the current device.  Errors as there. */
 SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args* args,
                                                  size_t* bytes);
+
+/*
+ * A paged cache of codes of `bits` bits (device memory).  Code c of an element of
+ * group j stands for o_j + s_j c, where the groups are the runs of `group`
+ * elements of a head's row and (s_j, o_j) is the row's j-th pair of fp16 numbers,
+ * scale and offset.
+ *   k, v   code pools.  The row of (page, token, head) starts at byte
+ *            page * page_stride + token * token_stride + head * head_stride
+ *          of either and holds head_dim * bits / 8 bytes: 16 units of
+ *          head_dim / 16 codes, unit w holding the codes of elements w, w + 16,
+ *          w + 32, ... from the lowest bits of its first byte up
+ *   k_scale, v_scale  pair pools.  The head_dim / group pairs of (page, token, head)
+ *          start at pair
+ *            page * scale_page_stride + token * scale_token_stride +
+ *            head * scale_head_stride
+ * Any order of heads and tokens within a page fits; heads outside of a page's
+ * tokens (a head's rows and pairs of a page in one run) reads fastest.
+ * head_dim 64, 128 or 256; bits 4 or 8; group 32, 64, 128 or 256, with one, two or
+ * four groups to a row.  The code pools are 16-byte aligned and their strides
+ * multiples of 16; the pair pools are aligned to a row's pairs and their strides
+ * are multiples of head_dim / group.  A code pool spans less than 2^36 bytes and a
+ * pair pool less than 2^32 rows.
+ */
+typedef struct seedlm_qcache_t {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int64_t pages;
+  int64_t page_stride, token_stride, head_stride;                   /* bytes */
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride; /* pairs */
+  int32_t page_size, kv_heads, head_dim, bits, group;
+} seedlm_qcache_t;
+
+/*
+ * seedlm_qcache_append -- seedlm_cache_append for a quantised cache: rotate q and k
+ * by their positions, write q_out, and quantise k and v into their slots.
+ * The arguments but `cache` are those of seedlm_cache_append, and so are padding
+ * rows.  k after its rotation (in fp32: two products and a sum, each rounded) and v
+ * are rounded to fp16; of a group of these values x
+ *   o = min x, s = fp16((max x - o) / (2^bits - 1)),
+ *   c = min(rint((x - o) / s), 2^bits - 1), or 0 where s is 0,
+ * so that a value reads back to s / 2 (and what s lost to its rounding).  A group
+ * with a NaN or an infinity (fp32 values that round to one among them) gets s = NaN:
+ * all of it reads back as NaN.
+ * One launch, no scratch.  tokens = 0 is a no-op.
+ * Errors: SEEDLM_E_INVALID (null, range, a stride smaller than what it spans),
+ * SEEDLM_E_UNSUPPORTED (dtype, odd rot, what the cache's fields above rule out, more
+ * than 16384 heads, tokens of 2^24 or more, pages * page_size of 2^31 or more),
+ * SEEDLM_E_DEVICE.
+ */
+typedef struct seedlm_qcache_append_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  const int32_t* slots;
+  seedlm_qcache_t cache;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int32_t tokens, heads, rot, table_len, interleaved, x_dtype;
+} seedlm_qcache_append_args;
+SEEDLM_API int seedlm_qcache_append(const seedlm_qcache_append_args* args, void* stream);
+
+/*
+ * seedlm_qcache_read -- what slots of a quantised cache stand for.
+ *   k_out, v_out  [tokens][kv_heads][head_dim] of y_dtype (SEEDLM_F32 or
+ *          SEEDLM_F16), row strides k_stride and v_stride elements, heads of a row
+ *          head_dim apart; either may be NULL.  o + s c in fp32, rounded once more
+ *          for fp16
+ *   slots  int32 [tokens]; a slot outside [0, pages * page_size) gives a row of
+ *          zeros; slots may repeat
+ * One launch, no scratch.  tokens = 0 is a no-op.
+ * Errors: SEEDLM_E_INVALID (null, range, a stride smaller than what it spans),
+ * SEEDLM_E_UNSUPPORTED (dtype, what the cache's fields rule out, more than 16384
+ * heads, tokens of 2^24 or more, pages * page_size of 2^31 or more),
+ * SEEDLM_E_DEVICE.
+ */
+typedef struct seedlm_qcache_read_args {
+  void* k_out;
+  void* v_out;
+  const int32_t* slots;
+  seedlm_qcache_t cache;
+  int64_t k_stride, v_stride;
+  int32_t tokens, y_dtype;
+} seedlm_qcache_read_args;
+SEEDLM_API int seedlm_qcache_read(const seedlm_qcache_read_args* args, void* stream);
+
+/*
+ * seedlm_qcache_attend -- seedlm_cache_attend for a quantised cache.  The arguments
+ * but `cache` are those of seedlm_cache_attend, and so are their bounds, lengths,
+ * rows and queries of no tokens.
+ * The codes enter the products as they are, exactly, and the pairs in fp32.  Scores,
+ * softmax statistics and sums are fp32; the softmax weights, times the values'
+ * scales, enter the matrix cores as the sum of two fp16 numbers (22 bits), as do
+ * fp32 queries, and fp16 queries exactly but for elements below 2^-20 of their row's
+ * largest.  A group whose pair is not finite among the keys that a query attends to
+ * makes its head's output NaN, among the values the elements of that group.  What
+ * lies in the cache beyond a query's length does not reach its output.
+ * Consecutive queries of one row share what they read of the cache.
+ * Scratch: seedlm_qcache_attend_scratch_bytes, on the stream.
+ * Results are the same for the same arguments; the split, and with it the
+ * order of sums, depends on all lengths of the call.
+ * Errors: SEEDLM_E_INVALID (null, range), SEEDLM_E_UNSUPPORTED (dtype, what the
+ * cache's fields rule out, alignment of q, size), SEEDLM_E_NOMEM, SEEDLM_E_DEVICE.
+ */
+typedef struct seedlm_qcache_attend_args {
+  const void* q;
+  void* out;
+  const int32_t* table;
+  const int32_t* rows;
+  const int32_t* lens;
+  seedlm_qcache_t cache;
+  int64_t q_stride, out_stride, table_stride;
+  int32_t queries, table_rows, heads, max_pages, max_len, x_dtype;
+  float scale;
+} seedlm_qcache_attend_args;
+SEEDLM_API int seedlm_qcache_attend(const seedlm_qcache_attend_args* args, void* stream);
+
+/* seedlm_qcache_attend_scratch_bytes -- stream scratch that seedlm_qcache_attend
+ * uses for these arguments on the current device.  Errors as there. */
+SEEDLM_API int seedlm_qcache_attend_scratch_bytes(const seedlm_qcache_attend_args* args,
+                                                  size_t* bytes);
 
 /*
  * seedlm_lora_many -- low-rank adapters of many requests beside shared

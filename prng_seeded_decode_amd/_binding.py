@@ -60,6 +60,10 @@ EXPORTED = (
     "seedlm_cache_append",
     "seedlm_cache_attend",
     "seedlm_cache_attend_scratch_bytes",
+    "seedlm_qcache_append",
+    "seedlm_qcache_read",
+    "seedlm_qcache_attend",
+    "seedlm_qcache_attend_scratch_bytes",
     "seedlm_lora_many",
     "seedlm_lora_scratch_bytes",
 )
@@ -129,6 +133,10 @@ def lib() -> ctypes.CDLL:
     L.seedlm_cache_append.argtypes = [vp, vp]
     L.seedlm_cache_attend.argtypes = [vp, vp]
     L.seedlm_cache_attend_scratch_bytes.argtypes = [vp, ctypes.POINTER(sz)]
+    L.seedlm_qcache_append.argtypes = [vp, vp]
+    L.seedlm_qcache_read.argtypes = [vp, vp]
+    L.seedlm_qcache_attend.argtypes = [vp, vp]
+    L.seedlm_qcache_attend_scratch_bytes.argtypes = [vp, ctypes.POINTER(sz)]
     L.seedlm_lora_many.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, vp]
     L.seedlm_lora_scratch_bytes.argtypes = [vp, i32, i64, i32, i32, i32, ctypes.POINTER(sz)]
     for name in EXPORTED:

@@ -47,6 +47,26 @@ class _AttendArgs(ctypes.Structure):
         ("x_dtype", _i32), ("scale", ctypes.c_float)]
 
 
+class _QCache(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, _i64) for n in ("pages", "page_stride", "token_stride", "head_stride",
+                            "scale_page_stride", "scale_token_stride", "scale_head_stride")] + [
+        (n, _i32) for n in ("page_size", "kv_heads", "head_dim", "bits", "group")]
+
+
+class _QAppendArgs(ctypes.Structure):
+    _fields_ = [("cache", _QCache) if f[0] == "cache" else f for f in _AppendArgs._fields_]
+
+
+class _QReadArgs(ctypes.Structure):
+    _fields_ = [("k_out", _vp), ("v_out", _vp), ("slots", _vp), ("cache", _QCache),
+                ("k_stride", _i64), ("v_stride", _i64), ("tokens", _i32), ("y_dtype", _i32)]
+
+
+class _QAttendArgs(ctypes.Structure):
+    _fields_ = [("cache", _QCache) if f[0] == "cache" else f for f in _AttendArgs._fields_]
+
+
 class _LoraSite(ctypes.Structure):
     _fields_ = [("x", _vp), ("A", _vp), ("B", _vp), ("base", _vp), ("y", _vp), ("rows", _i64),
                 ("cols", _i64), ("rank", _i32)]
@@ -106,6 +126,94 @@ def _cache(k_cache, v_cache):
         raise ValueError("both caches must have the same shape and strides")
     pages, size, heads, dim = k_cache.shape
     return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), pages, *strides[0], size, heads, dim)
+
+
+def _qcache(k_cache, v_cache, k_scale, v_scale, dim):
+    import torch
+
+    for t in (k_cache, v_cache):
+        if t.dtype != torch.uint8 or t.dim() != 4:
+            raise ValueError("the caches must be uint8 [pages][page_size][kv_heads][bytes of a row]")
+        if t.shape[3] > 1 and t.stride(3) != 1:
+            raise ValueError("the bytes of a row must be contiguous in the caches")
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float16 or t.dim() != 5 or t.shape[4] != 2:
+            raise ValueError("the scales must be float16 [pages][page_size][kv_heads][groups][2]")
+        if t.stride(4) != 1 or (t.shape[3] > 1 and t.stride(3) != 2):
+            raise ValueError("the pairs of a row must be contiguous in the scales")
+    if k_scale.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("caches and scales must have the same pages, page_size and kv_heads")
+    # the stride of a dimension of one entry says nothing
+    at = [[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+          for t in (k_cache, v_cache, k_scale, v_scale)]
+    if k_cache.shape != v_cache.shape or k_scale.shape != v_scale.shape or at[0] != at[1] or at[2] != at[3]:
+        raise ValueError("keys and values must have the same shapes and strides")
+    if any(s % 2 for s in at[2]):
+        raise ValueError("the strides of the scales must be whole pairs")
+    pages, size, heads, width = k_cache.shape
+    groups = k_scale.shape[3]
+    if groups == 0 or dim % groups or width * 8 % dim:
+        raise ValueError("rows and scales do not fit head_dim")
+    return _QCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   pages, *at[0], *(s // 2 for s in at[2]), size, heads, dim, width * 8 // dim,
+                   dim // groups)
+
+
+def _append_args(struct, cache, q, k, v, cos, sin, positions, slots, q_out, interleaved):
+    """The arguments of an append call, into either cache."""
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens][heads][head_dim]")
+    tokens, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError("q and the caches must have the same head_dim")
+    for t in (cos, sin):
+        if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 [table_len][rot / 2]")
+    if cos.shape != sin.shape:
+        raise ValueError("cos and sin must have the same shape")
+    code = _dtype_code(q)
+    strides = [_heads("q", q, tokens, heads, dim, q.dtype),
+               _heads("k", k, tokens, cache.kv_heads, dim, q.dtype),
+               _heads("v", v, tokens, cache.kv_heads, dim, q.dtype),
+               _heads("q_out", q_out, tokens, heads, dim, q.dtype)]
+    return struct(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), cos.data_ptr(),
+        sin.data_ptr(), _ints("positions", positions, tokens), _ints("slots", slots, tokens),
+        cache, *strides, tokens, heads, 2 * cos.shape[1], cos.shape[0],
+        int(bool(interleaved)), code)
+
+
+def _attend_args(struct, cache, q, table, lens, out, scale, max_len, rows):
+    """The arguments of an attention call, over either cache."""
+    if q.dim() != 3:
+        raise ValueError("q must be [queries][heads][head_dim]")
+    n, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError("q and the caches must have the same head_dim")
+    at, max_pages, stride = _table(table)
+    if rows is None and table.shape[0] < n:
+        raise ValueError("without rows, table must have a row for each query")
+    code = _dtype_code(q)
+    room = min(max_pages * cache.page_size, _INT32_MAX)
+    if max_len is not None and max_len < 0:
+        raise ValueError("max_len must not be negative")
+    return struct(
+        q.data_ptr(), out.data_ptr(), at, None if rows is None else _ints("rows", rows, n),
+        _ints("lens", lens, n), cache,
+        _heads("q", q, n, heads, dim, q.dtype), _heads("out", out, n, heads, dim, q.dtype),
+        stride, n, table.shape[0], heads, max_pages,
+        room if max_len is None else min(max_len, room), code,
+        dim ** -0.5 if scale is None else scale)
+
+
+def _scratch(name, args):
+    n = ctypes.c_size_t(0)
+    st = getattr(lib(), name)(ctypes.byref(args), ctypes.byref(n))
+    if st != OK:
+        raise SeedLMError(st, name)
+    return n.value
 
 
 class _Call:
@@ -171,31 +279,10 @@ class CacheAppendCall(_Call):
 
     def __init__(self, q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache,
                  interleaved=False, stream=None):
-        import torch
-
         keep = (q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache)
         device = _on_device(keep)
-        cache = _cache(k_cache, v_cache)
-        if q.dim() != 3:
-            raise ValueError("q must be [tokens][heads][head_dim]")
-        tokens, heads, dim = q.shape
-        if dim != cache.head_dim:
-            raise ValueError("q and the caches must have the same head_dim")
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous float32 [table_len][rot / 2]")
-        if cos.shape != sin.shape:
-            raise ValueError("cos and sin must have the same shape")
-        code = _dtype_code(q)
-        strides = [_heads("q", q, tokens, heads, dim, q.dtype),
-                   _heads("k", k, tokens, cache.kv_heads, dim, q.dtype),
-                   _heads("v", v, tokens, cache.kv_heads, dim, q.dtype),
-                   _heads("q_out", q_out, tokens, heads, dim, q.dtype)]
-        args = _AppendArgs(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), cos.data_ptr(),
-            sin.data_ptr(), _ints("positions", positions, tokens), _ints("slots", slots, tokens),
-            cache, *strides, tokens, heads, 2 * cos.shape[1], cos.shape[0],
-            int(bool(interleaved)), code)
+        args = _append_args(_AppendArgs, _cache(k_cache, v_cache), q, k, v, cos, sin, positions,
+                            slots, q_out, interleaved)
         self._set("seedlm_cache_append", lib().seedlm_cache_append, (ctypes.byref(args),), keep,
                   device, stream)
 
@@ -214,37 +301,83 @@ class CacheAttendCall(_Call):
                  stream=None, rows=None):
         keep = (q, k_cache, v_cache, table, lens, out) + (() if rows is None else (rows,))
         device = _on_device(keep)
-        cache = _cache(k_cache, v_cache)
-        if q.dim() != 3:
-            raise ValueError("q must be [queries][heads][head_dim]")
-        n, heads, dim = q.shape
-        if dim != cache.head_dim:
-            raise ValueError("q and the caches must have the same head_dim")
-        at, max_pages, stride = _table(table)
-        if rows is None and table.shape[0] < n:
-            raise ValueError("without rows, table must have a row for each query")
-        code = _dtype_code(q)
-        room = min(max_pages * cache.page_size, _INT32_MAX)
-        if max_len is not None and max_len < 0:
-            raise ValueError("max_len must not be negative")
-        args = _AttendArgs(
-            q.data_ptr(), out.data_ptr(), at, None if rows is None else _ints("rows", rows, n),
-            _ints("lens", lens, n), cache,
-            _heads("q", q, n, heads, dim, q.dtype), _heads("out", out, n, heads, dim, q.dtype),
-            stride, n, table.shape[0], heads, max_pages,
-            room if max_len is None else min(max_len, room), code,
-            dim ** -0.5 if scale is None else scale)
+        args = _attend_args(_AttendArgs, _cache(k_cache, v_cache), q, table, lens, out, scale,
+                            max_len, rows)
         self._set("seedlm_cache_attend", lib().seedlm_cache_attend, (ctypes.byref(args),), keep,
                   device, stream)
         self._struct = args
 
     def scratch_bytes(self) -> int:
         """Stream scratch that the call uses."""
-        n = ctypes.c_size_t(0)
-        st = lib().seedlm_cache_attend_scratch_bytes(ctypes.byref(self._struct), ctypes.byref(n))
-        if st != OK:
-            raise SeedLMError(st, "seedlm_cache_attend_scratch_bytes")
-        return n.value
+        return _scratch("seedlm_cache_attend_scratch_bytes", self._struct)
+
+
+class QCacheAppendCall(_Call):
+    """Rotary positions on q and k, q_out, and k and v quantised into their cache slots
+    (seedlm_qcache_append).
+
+    The arguments are CacheAppendCall's but for the caches: k_cache, v_cache: uint8
+    [pages][page_size][kv_heads][head_dim * bits / 8], bits 4 or 8; k_scale, v_scale: float16
+    [pages][page_size][kv_heads][groups][2], the (scale, offset) of each of a row's 1, 2 or 4
+    groups of at least 32 elements.  Any strides but within a row, those of the caches multiples
+    of 16; pools made as [pages][kv_heads][page_size][...] and transposed read fastest."""
+
+    def __init__(self, q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, k_scale,
+                 v_scale, interleaved=False, stream=None):
+        keep = (q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, k_scale, v_scale)
+        device = _on_device(keep)
+        cache = _qcache(k_cache, v_cache, k_scale, v_scale, q.shape[-1])
+        args = _append_args(_QAppendArgs, cache, q, k, v, cos, sin, positions, slots, q_out,
+                            interleaved)
+        self._set("seedlm_qcache_append", lib().seedlm_qcache_append, (ctypes.byref(args),), keep,
+                  device, stream)
+
+
+class QCacheReadCall(_Call):
+    """What slots of a quantised cache stand for (seedlm_qcache_read).
+
+    k_cache, v_cache, k_scale, v_scale: as for QCacheAppendCall; slots: int32 [tokens], outside
+    the cache for a row of zeros; k_out, v_out: [tokens][kv_heads][head_dim], float16 or float32,
+    their rows contiguous; either may be None."""
+
+    def __init__(self, k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, stream=None):
+        outs = [t for t in (k_out, v_out) if t is not None]
+        if not outs:
+            raise ValueError("k_out or v_out must be given")
+        keep = (k_cache, v_cache, k_scale, v_scale, slots, *outs)
+        device = _on_device(keep)
+        cache = _qcache(k_cache, v_cache, k_scale, v_scale, outs[0].shape[-1])
+        code, tokens = _dtype_code(outs[0]), slots.numel()
+        strides = [0 if t is None else _heads(what, t, tokens, cache.kv_heads, cache.head_dim,
+                                              outs[0].dtype)
+                   for what, t in (("k_out", k_out), ("v_out", v_out))]
+        args = _QReadArgs(*(None if t is None else t.data_ptr() for t in (k_out, v_out)),
+                          _ints("slots", slots, tokens), cache, *strides, tokens, code)
+        self._set("seedlm_qcache_read", lib().seedlm_qcache_read, (ctypes.byref(args),), keep,
+                  device, stream)
+
+
+class QCacheAttendCall(_Call):
+    """Attention of query tokens over their requests' pages of a quantised cache
+    (seedlm_qcache_attend).
+
+    The arguments are CacheAttendCall's but for the caches, which are QCacheAppendCall's.
+    Consecutive queries of one row share what they read of the cache."""
+
+    def __init__(self, q, k_cache, v_cache, k_scale, v_scale, table, lens, out, scale=None,
+                 max_len=None, stream=None, rows=None):
+        keep = (q, k_cache, v_cache, k_scale, v_scale, table, lens, out) + (
+            () if rows is None else (rows,))
+        device = _on_device(keep)
+        cache = _qcache(k_cache, v_cache, k_scale, v_scale, q.shape[-1])
+        args = _attend_args(_QAttendArgs, cache, q, table, lens, out, scale, max_len, rows)
+        self._set("seedlm_qcache_attend", lib().seedlm_qcache_attend, (ctypes.byref(args),), keep,
+                  device, stream)
+        self._struct = args
+
+    def scratch_bytes(self) -> int:
+        """Stream scratch that the call uses."""
+        return _scratch("seedlm_qcache_attend_scratch_bytes", self._struct)
 
 
 class LoraCall(_Call):
@@ -321,6 +454,28 @@ def seedlm_cache_attend(q, k_cache, v_cache, table, lens, out, scale=None, max_l
                         stream=None, rows=None):
     """One call of CacheAttendCall; returns out."""
     CacheAttendCall(q, k_cache, v_cache, table, lens, out, scale, max_len, stream, rows)()
+    return out
+
+
+def seedlm_qcache_append(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, k_scale,
+                         v_scale, interleaved=False, stream=None):
+    """One call of QCacheAppendCall; returns q_out."""
+    QCacheAppendCall(q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, k_scale, v_scale,
+                     interleaved, stream)()
+    return q_out
+
+
+def seedlm_qcache_read(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, stream=None):
+    """One call of QCacheReadCall; returns (k_out, v_out)."""
+    QCacheReadCall(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out, stream)()
+    return k_out, v_out
+
+
+def seedlm_qcache_attend(q, k_cache, v_cache, k_scale, v_scale, table, lens, out, scale=None,
+                         max_len=None, stream=None, rows=None):
+    """One call of QCacheAttendCall; returns out."""
+    QCacheAttendCall(q, k_cache, v_cache, k_scale, v_scale, table, lens, out, scale, max_len, stream,
+                     rows)()
     return out
 
 

@@ -173,6 +173,10 @@ int launch_cache_plan(const seedlm_cache_plan_args& a, int32_t* scratch, hipStre
 int launch_cache_append(const seedlm_cache_append_args& a, hipStream_t s);
 size_t cache_attend_scratch_bytes(const seedlm_cache_attend_args& a);
 int launch_cache_attend(const seedlm_cache_attend_args& a, void* scratch, hipStream_t s);
+int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s);
+int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s);
+size_t qcache_attend_scratch_bytes(const seedlm_qcache_attend_args& a);
+int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipStream_t s);
 constexpr int kLoraGroup = 8;  // sites of one pair of launches
 size_t lora_scratch_bytes(const seedlm_lora_site* sites, int n, int64_t tokens, int adapters,
                           int xdt, int ydt);
