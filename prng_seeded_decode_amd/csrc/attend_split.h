@@ -1,0 +1,70 @@
+// What the attention kernels share: how the work of requests of any lengths is cut
+// into even runs of units, and page numbers without a division.
+#pragma once
+
+#include "seedlm_internal.h"
+
+namespace seedlm {
+
+// The first unit of a slot among `units`, and the slot of a unit: the largest i
+// with i * units / slots <= u, that is i * units < (u + 1) * slots.
+__device__ inline int slot_begin(int slot, int units, int slots) {
+  return (int)((int64_t)slot * units / slots);
+}
+__device__ inline int slot_of(int u, int units, int slots) {
+  return (int)((((int64_t)u + 1) * slots - 1) / units);
+}
+
+// Inclusive sums of units_of(0), ..., units_of(n - 1) into ends[0..n), by all
+// THREADS threads, each taking consecutive numbers.
+template <int THREADS, typename F>
+__device__ void sum_units(int n, int32_t* ends, F units_of) {
+  __shared__ int s_wave[THREADS / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = (n + THREADS - 1) / THREADS;
+  const int b0 = min((int)threadIdx.x * per, n), b1 = min(b0 + per, n);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    mine += units_of(b);
+    ends[b] = mine;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 63) s_wave[wave] = upto;
+  __syncthreads();
+  int before = upto - mine;
+  for (int w = 0; w < wave; ++w) before += s_wave[w];
+  for (int b = b0; b < b1; ++b) ends[b] += before;
+  __syncthreads();
+}
+
+// The first request whose inclusive sum exceeds u.
+__device__ inline int request_of(const int32_t* ends, int n, int u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > u) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// x / d for 0 <= x < 2^31, with 2^(L-1) < d <= 2^L: ceil(2^(31+L) / d) is less
+// than 1 above 2^(31+L) / d, so the product is less than x / 2^(31+L) < 2^-L
+// above x / d.  That is at most 1/d, which no quotient's fraction lacks less
+// than to the next whole number, so the floor is the quotient's.
+struct Divisor {
+  uint32_t mul, shift;
+  __device__ uint32_t of(uint32_t x) const { return (uint32_t)(((uint64_t)x * mul) >> shift); }
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t L = 0;
+  while (((uint64_t)1 << L) < d) ++L;
+  return {(uint32_t)((((uint64_t)1 << (31 + L)) + d - 1) / d), 31 + L};
+}
+
+}  // namespace seedlm

@@ -50,7 +50,7 @@
 
 #include <type_traits>
 
-#include "seedlm_internal.h"
+#include "attend_split.h"
 
 namespace seedlm {
 namespace {
@@ -74,7 +74,7 @@ struct AttendArgs {
   int slots;            // runs of units; 0: one workgroup per request
   int cap;              // largest length: min(max_len, max_pages * page_size)
   uint32_t page_unit, token_unit;  // strides in units of 8 elements
-  uint32_t div_mul, div_shift;     // x / page_size = x * div_mul >> div_shift
+  Divisor page_size;
   int32_t* ends;        // [requests] inclusive sums of units, for the join
   float2* ml;           // [2 * slots][heads] maximum (log2) and sum
   float* acc;           // [2 * slots][heads][D]
@@ -84,52 +84,6 @@ struct AttendArgs {
 __device__ int length_of(const AttendArgs& p, int b) {
   const int len = min(max(p.a.lens[b], 0), p.cap);
   return !p.a.rows || (uint32_t)p.a.rows[b] < (uint32_t)p.a.table_rows ? len : 0;
-}
-
-// The first unit of a slot among `units`, and the slot of a unit: the largest i
-// with i * units / slots <= u, that is i * units < (u + 1) * slots.
-__device__ int slot_begin(int slot, int units, int slots) {
-  return (int)((int64_t)slot * units / slots);
-}
-__device__ int slot_of(int u, int units, int slots) {
-  return (int)((((int64_t)u + 1) * slots - 1) / units);
-}
-
-// Inclusive sums of the requests' units into ends[0..n), by all threads, each
-// taking consecutive requests.
-__device__ void sum_units(const AttendArgs& p, int32_t* ends) {
-  __shared__ int s_wave[kWaves];
-  const int n = p.a.queries, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int per = (n + kThreads - 1) / kThreads;
-  const int b0 = min((int)threadIdx.x * per, n), b1 = min(b0 + per, n);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    mine += (length_of(p, b) + kUnit - 1) / kUnit;
-    ends[b] = mine;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(upto, d);
-    if (lane >= d) upto += v;
-  }
-  if (lane == 63) s_wave[wave] = upto;
-  __syncthreads();
-  int before = upto - mine;
-  for (int w = 0; w < wave; ++w) before += s_wave[w];
-  for (int b = b0; b < b1; ++b) ends[b] += before;
-  __syncthreads();
-}
-
-// The first request whose inclusive sum exceeds u.
-__device__ int request_of(const int32_t* ends, int n, int u) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ends[mid] > u) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
 }
 
 __device__ half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
@@ -182,7 +136,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D)) void attend_kernel(con
   extern __shared__ int32_t s_ends[];  // of the requests' units
   int unit = 0, unit_end = 1, run_begin = 0;
   if (p.slots > 0) {
-    sum_units(p, s_ends);
+    sum_units<kThreads>(a.queries, s_ends,
+                        [&](int b) { return (length_of(p, b) + kUnit - 1) / kUnit; });
     const int units = s_ends[a.queries - 1];
     if (blockIdx.x == 0 && blockIdx.y == 0)
       for (int b = threadIdx.x; b < a.queries; b += kThreads) p.ends[b] = s_ends[b];
@@ -266,7 +221,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D)) void attend_kernel(con
       const int tok = first + i * kUnit + (lane & 31);
       page = -1;
       if (tok < end) {
-        const uint32_t nr = (uint32_t)(((uint64_t)(uint32_t)tok * p.div_mul) >> p.div_shift);
+        const uint32_t nr = p.page_size.of(tok);
         nth = tok - (int)nr * a.cache.page_size;
         page = table[nr];
       }
@@ -589,15 +544,7 @@ int launch_cache_attend(const seedlm_cache_attend_args& a, void* scratch, hipStr
   p.cap = cap_of(a);
   p.page_unit = (uint32_t)(a.cache.page_stride / 8);
   p.token_unit = (uint32_t)(a.cache.token_stride / 8);
-  // x / d for 0 <= x < 2^31, with 2^(L-1) < d <= 2^L: ceil(2^(31+L) / d) is less
-  // than 1 above 2^(31+L) / d, so the product is less than x / 2^(31+L) < 2^-L
-  // above x / d.  That is at most 1/d, which no quotient's fraction lacks less
-  // than to the next whole number, so the floor is the quotient's.
-  const uint32_t d = (uint32_t)a.cache.page_size;
-  uint32_t L = 0;
-  while (((uint64_t)1 << L) < d) ++L;
-  p.div_mul = (uint32_t)((((uint64_t)1 << (31 + L)) + d - 1) / d);
-  p.div_shift = 31 + L;
+  p.page_size = divisor(a.cache.page_size);
   const Scratch r = scratch_of(a);
   char* base = static_cast<char*>(scratch);
   if (base) {

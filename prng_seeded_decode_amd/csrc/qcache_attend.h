@@ -1,0 +1,635 @@
+// Attention of query tokens over their requests' pages of a quantised cache
+// (seedlm_qcache_attend): out = sum_t softmax_t(scale q . k_t) v_t, where element d of
+// k_t is o_tj + s_tj c_td with j the group of d, and v_t likewise.
+//
+// Mathematics.  The codes go into the matrix products as they are:
+//   q . k_t     = sum_j (s_tj sum_{d in j} q_d c_td + o_tj sum_{d in j} q_d)
+//   sum_t p_t v_td = sum_t (p_t s_tj) c_td + sum_t p_t o_tj
+// so a group costs its pair's products and not a multiplication per element, and
+// nothing is rounded on the way.  A code in the low bits of an fp16 number is the
+// subnormal c 2^-24, which the matrix cores take exactly: a mask and at most a byte
+// permutation unpack two codes.  Bits 4 to 7 hold 16 c 2^-24; the query elements that
+// meet those are divided by 16, and so are the outputs that come of them.
+//
+// Split.  As in cache_attend.hip: the 128-token units of all items, one after another,
+// are cut into even runs, one per workgroup and cache head, and what is cut is joined by
+// qcache_attend_join_kernel; short calls are not split.  An item is one query, or
+// where rows are given up to 16 / group consecutive queries of one row: their heads share
+// the 16 columns of the matrix products and what is read and unpacked.
+//
+// Tile.  A wave takes 32 tokens:
+//   S^T = K Q^T   A = 16 tokens' codes, B = 16 columns: lane l gets column l%16, tokens
+//                 4(l/16)+i.  Lane l holds units 4(l/16)..+3 of token l%16, and product
+//                 step c contracts the codes 2c and 2c+1 of all units, elements 32c to
+//                 32c+31: a group is whole steps and its sum comes out by itself.
+//   O^T = V^T P^T A = code i of unit l%16 of 8 tokens, the ones that lane l holds scores
+//                 of, B = their weights: element 16i + l%16, so a group is whole products
+//                 and each has its own weights p s.
+// Tile i+1's codes and pairs are requested before tile i is computed, its page numbers one
+// tile earlier still and before those loads (a wait for a load is one for all before it).
+// Pairs pass through LDS, where 4 tokens' are one read.
+//
+// Precision.  p s enters the second product as the sum of two fp16 numbers (22 bits).
+// Values' scales may have any fp16 exponent, so the running maximum is taken of
+// x + E with 2^E above every scale so far: weights stay below 2^15.
+#pragma once
+
+#include <hip/hip_fp16.h>
+
+#include <type_traits>
+
+#include "attend_split.h"
+
+namespace seedlm {
+namespace qattend {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kTile = 32;              // tokens of a wave's step
+constexpr int kUnit = kWaves * kTile;  // tokens of a workgroup's step
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Args {
+  seedlm_qcache_attend_args a;
+  int group;    // query heads per cache head
+  int qtiles;   // ceil(group / 16)
+  int shared;   // queries of an item at most
+  int slots;    // runs of units; 0: one workgroup per item
+  int cap;      // largest length: min(max_len, max_pages * page_size)
+  uint32_t page_unit, token_unit;  // strides of codes in units of 16 bytes
+  uint32_t page_pair, token_pair;  // strides of pairs in rows of pairs
+  Divisor page_size;
+  int32_t* ends;  // [queries] inclusive sums of units, for the join
+  float2* ml;     // [2 * slots][kv_heads * qtiles][16] maximum (log2) and sum
+  float* acc;     // [2 * slots][kv_heads * qtiles][16][D]
+};
+
+// A query's tokens; 0 for one without a row of the table.
+__device__ inline int length_of(const Args& p, int b) {
+  const int len = min(max(p.a.lens[b], 0), p.cap);
+  return !p.a.rows || (uint32_t)p.a.rows[b] < (uint32_t)p.a.table_rows ? len : 0;
+}
+
+// Whether query b is the first of its item.
+__device__ inline bool starts_item(const Args& p, int b) {
+  return p.shared == 1 || b % p.shared == 0 || p.a.rows[b] != p.a.rows[b - 1];
+}
+
+// The queries of the item that starts with b, and the longest of their lengths.
+__device__ inline int2 item_of(const Args& p, int b) {
+  int n = 1, len = length_of(p, b);
+  while (b + n < p.a.queries && !starts_item(p, b + n)) len = max(len, length_of(p, b + n)), ++n;
+  return make_int2(n, len);
+}
+
+__device__ inline half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
+__device__ inline half2v as_half2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
+
+__device__ inline uint32_t pack_rtz(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+}
+
+template <typename T>
+__device__ void store4(T* p, floatx4 v) {
+  if constexpr (sizeof(T) == 4) {
+    p[0] = v[0], p[1] = v[1], p[2] = v[2], p[3] = v[3];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __float2half_rn(v[i]);
+  }
+}
+
+// Byte n of a and of b in the low bytes of the two halves; the bytes above them are 0.
+__device__ inline uint32_t pair_bytes(uint32_t a, uint32_t b, int n) {
+  return __builtin_amdgcn_perm(b, a, 0x0C040C00u + 0x00010001u * n);
+}
+
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // codes c and 16 c of two bytes
+
+template <int D, int BITS>
+struct Row {
+  static constexpr int kBytes = D * BITS / 8;
+  static constexpr int kUnitBytes = kBytes / 16;
+  static constexpr int KD = kBytes / 16;                             // dwords of 4 units
+  static constexpr int VD = kUnitBytes < 4 ? 1 : kUnitBytes / 4;     // dwords of a unit
+  static constexpr int kSteps = D / 32, kAccs = D / 16;
+
+  // The operand of step c from 4 units of a token: (u0, u1) code 2c, (u0, u1) code
+  // 2c + 1, (u2, u3) code 2c, (u2, u3) code 2c + 1.
+  __device__ static half8 keys(const uint32_t (&k)[KD], int c) {
+    v4u r;
+    if constexpr (BITS == 8) {
+      const int d = c / 2, n = 2 * (c % 2);
+      r = v4u{pair_bytes(k[d], k[VD + d], n), pair_bytes(k[d], k[VD + d], n + 1),
+              pair_bytes(k[2 * VD + d], k[3 * VD + d], n),
+              pair_bytes(k[2 * VD + d], k[3 * VD + d], n + 1)};
+    } else {
+      uint32_t lo, hi;
+      if constexpr (kUnitBytes == 2) {  // two units to a dword
+        lo = k[0] >> (8 * c), hi = k[1] >> (8 * c);
+      } else {
+        const int d = c / 4, n = c % 4;
+        lo = pair_bytes(k[d], k[VD + d], n), hi = pair_bytes(k[2 * VD + d], k[3 * VD + d], n);
+      }
+      r = v4u{lo & kLow, lo & kHigh, hi & kLow, hi & kHigh};
+    }
+    return as_half8(r);
+  }
+
+  // The operand of code i from a unit of 8 tokens.
+  __device__ static half8 values(const uint32_t (&v)[8][VD], int i) {
+    v4u r;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int byte = i * BITS / 8;
+      const uint32_t b = pair_bytes(v[2 * x][byte / 4], v[2 * x + 1][byte / 4], byte % 4);
+      r[x] = BITS == 8 ? b : b & (i % 2 ? kHigh : kLow);
+    }
+    return as_half8(r);
+  }
+
+  // The operand of keys() whose codes are all 1.
+  __device__ static half8 ones() {
+    const uint32_t odd = BITS == 8 ? 0x00010001u : 0x00100010u;
+    return as_half8(v4u{0x00010001u, odd, 0x00010001u, odd});
+  }
+};
+
+// Bytes [at, at + 4 N) as N dwords, or 2 bytes as one.
+template <int BYTES, int N>
+__device__ void load_codes(const uint8_t* p, uint32_t (&out)[N]) {
+  if constexpr (BYTES == 2) {
+    out[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else if constexpr (BYTES == 4) {
+    out[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (BYTES == 8) {
+    const v2u v = *reinterpret_cast<const v2u*>(p);
+    out[0] = v[0], out[1] = v[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const v4u v = reinterpret_cast<const v4u*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[4 * i + j] = v[j];
+    }
+  }
+}
+
+// Waves of the kernel per SIMD, and so workgroups per compute unit: what the registers
+// of each form allow.
+__host__ __device__ constexpr int waves_per_simd(int D, int bits, bool wide) {
+  return D == 256 ? (bits == 8 ? 1 : 2) : (D == 128 && (bits == 8 || wide) ? 2 : 3);
+}
+
+template <int D, int BITS, int NG, bool WIDE>
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcache_attend_kernel(
+    const Args p) {
+  using T = std::conditional_t<WIDE, float, __half>;
+  using R = Row<D, BITS>;
+  constexpr int kSteps = R::kSteps, kAccs = R::kAccs, KD = R::KD, VD = R::VD;
+  constexpr int kStride = D + 4;  // LDS row stride (floats)
+  __shared__ __align__(16) uint32_t s_off[kWaves][kTile];
+  __shared__ __align__(16) uint32_t s_pair[kWaves][2 * kTile * NG];
+  __shared__ float2 s_ml[kWaves][16];
+  __shared__ __align__(16) float s_acc[kWaves][16][kStride];
+  extern __shared__ int32_t s_ends[];  // of the items' units
+  const seedlm_qcache_attend_args& a = p.a;
+  const seedlm_qcache_t& c = a.cache;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int m = lane & 15, g = lane >> 4;
+  const int hk = blockIdx.x / p.qtiles, qt = blockIdx.x % p.qtiles;
+  const int heads = min(16, p.group - qt * 16);  // of a query in this tile
+  const int head0 = hk * p.group + qt * 16;
+
+  int unit = 0, unit_end = 1, run_begin = 0;
+  if (p.slots > 0) {
+    sum_units<kThreads>(a.queries, s_ends, [&](int b) {
+      return starts_item(p, b) ? (item_of(p, b).y + kUnit - 1) / kUnit : 0;
+    });
+    const int units = s_ends[a.queries - 1];
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+      for (int b = threadIdx.x; b < a.queries; b += kThreads) p.ends[b] = s_ends[b];
+    const int slots = min(p.slots, units);  // none is empty
+    if ((int)blockIdx.y >= slots) return;
+    run_begin = unit = slot_begin(blockIdx.y, units, slots);
+    unit_end = slot_begin(blockIdx.y + 1, units, slots);
+  } else if (!starts_item(p, blockIdx.y)) {
+    return;
+  }
+  while (unit < unit_end) {
+    // The next item of the run and the tokens of it that lie in the run.
+    int first_query = blockIdx.y, begin = 0, end;
+    bool whole = true;
+    const bool starts_run = unit == run_begin;
+    if (p.slots > 0) first_query = request_of(s_ends, a.queries, unit);
+    const int2 item = item_of(p, first_query);
+    if (p.slots > 0) {
+      const int u0 = first_query > 0 ? s_ends[first_query - 1] : 0, u1 = s_ends[first_query];
+      const int upto = min(u1, unit_end);
+      begin = (unit - u0) * kUnit;
+      end = min(item.y, (upto - u0) * kUnit);
+      whole = unit == u0 && upto == u1;
+      unit = upto;
+    } else {
+      end = item.y;
+      unit = unit_end;
+    }
+
+    // This lane's column: a query and a head.
+    const int columns = item.x * heads;
+    const int column = min(m, columns - 1);
+    const int query = first_query + column / heads, head = head0 + column % heads;
+    const int length = m < columns ? length_of(p, query) : item.y;
+
+    // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
+    // (0..3), in the order of Row::keys.  The row's largest element goes into [2^9, 2^10),
+    // so that low parts and sixteenths have all their bits.
+    half8 qh[kSteps], ql[WIDE ? kSteps : 1];
+    float sc = a.scale * kLog2e;
+    float qsum[NG];  // of a group's elements, in the units of its products with codes
+    {
+      const T* q = static_cast<const T*>(a.q) + (int64_t)query * a.q_stride + (int64_t)head * D + g * 4;
+      float f[kSteps][8], top = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[s][(j / 2) * 4 + h * 2 + j % 2] = (float)q[16 * (2 * s + h) + j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[s][j]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      int e = 10;
+      if (top > 0.f && top < INFINITY) (void)frexpf(top, &e);
+      const int up = 10 - e;
+      sc = ldexpf(sc, 24 - up);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = m < columns ? ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up) : 0.f;
+          qh[s][j] = (_Float16)x;
+          if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
+        }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = j * kSteps / NG; i < (j + 1) * kSteps / NG; ++i) {
+          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), qh[i], s, 0, 0, 0);
+          if constexpr (WIDE) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), ql[i], s, 0, 0, 0);
+        }
+        qsum[j] = s[0];
+      }
+    }
+
+    const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
+    const uint8_t* vbase = static_cast<const uint8_t*>(c.v) + hk * c.head_stride + m * R::kUnitBytes;
+    // lanes 0..31 fetch the keys' pairs of the tile's tokens, lanes 32..63 the values'
+    const uint32_t* pairs = static_cast<const uint32_t*>(lane < kTile ? c.k_scale : c.v_scale) +
+                            hk * c.scale_head_stride;
+    const int32_t* table = a.table + (a.rows ? (int64_t)a.rows[first_query] : first_query) * a.table_stride;
+
+    // Tile i of this wave: tokens first + 128 i + (0..31); lane l looks after token l % 32.
+    const int first = begin + wave * kTile;
+    const int tiles = first < end ? (end - first + kUnit - 1) / kUnit : 0;
+    int page = -1, nth = 0;  // of this lane's token in the tile after the next
+    auto look_up = [&](int i) {
+      const int tok = first + i * kUnit + (lane & 31);
+      page = -1;
+      if (tok < end) {
+        const uint32_t nr = p.page_size.of(tok);
+        nth = tok - (int)nr * c.page_size;
+        page = table[nr];
+      }
+    };
+    struct Tile {
+      uint32_t k[2][KD], v[8][VD], pair[NG];
+      uint32_t live;  // bit j: this lane's token j of the tile exists
+      bool ok;        // this lane's token exists
+      bool whole;     // all tokens exist
+    };
+    // Requests the tile that was looked up, and looks up tile `next`.
+    auto request = [&](Tile& t, int next) {
+      const bool ok = (uint32_t)page < (uint32_t)c.pages;
+      const uint32_t off = (uint32_t)page * p.page_unit + (uint32_t)nth * p.token_unit;
+      const uint32_t row = ok ? (uint32_t)page * p.page_pair + (uint32_t)nth * p.token_pair : 0;
+      if (lane < kTile) s_off[wave][lane] = ok ? off : kNoToken;
+      if (next < tiles) look_up(next);
+      t.ok = ok;
+      t.whole = !__any(!ok);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      uint32_t koff[2] = {s_off[wave][m], s_off[wave][16 + m]};
+      const v4u o[2] = {*reinterpret_cast<const v4u*>(&s_off[wave][4 * g]),
+                        *reinterpret_cast<const v4u*>(&s_off[wave][16 + 4 * g])};
+      uint32_t voff[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) voff[j] = o[j >> 2][j & 3];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      t.live = 0xFF;
+      if (!t.whole) {  // tokens that do not exist read token 0 of page 0 and are masked
+        t.live = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          t.live |= (voff[j] != kNoToken) << j;
+          voff[j] = voff[j] != kNoToken ? voff[j] : 0;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) koff[h] = koff[h] != kNoToken ? koff[h] : 0;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_codes<R::kBytes / 4>(kbase + (uint64_t)koff[h] * 16, t.k[h]);
+      load_codes<4 * NG>(reinterpret_cast<const uint8_t*>(pairs + (uint64_t)row * NG), t.pair);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) load_codes<R::kUnitBytes>(vbase + (uint64_t)voff[j] * 16, t.v[j]);
+    };
+
+    float top = -INFINITY, base = -INFINITY;  // running maximum (log2), and with E added
+    float sum = 0.f, osum[NG];  // this lane's share of the weights, and of them times offsets
+    floatx4 acc[kAccs];
+    uint32_t largest = 0;  // exponent bits of the largest scale so far
+    float E = -14.f;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) osum[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAccs; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    auto compute = [&](const Tile& t, int i) {
+      floatx4 s[NG][2];
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s[j][h] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = j * kSteps / NG; k < (j + 1) * kSteps / NG; ++k) {
+            const half8 x = R::keys(t.k[h], k);
+            s[j][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, qh[k], s[j][h], 0, 0, 0);
+            if constexpr (WIDE)
+              s[j][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, ql[k], s[j][h], 0, 0, 0);
+          }
+        }
+      // Pairs: none of a token that does not exist, NaN for what is not finite.
+      uint32_t e = 0;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        uint32_t x = t.ok ? t.pair[j] : 0;
+        const uint32_t es = x & 0x7C00u, eo = x & 0x7C000000u;
+        if (es == 0x7C00u || eo == 0x7C000000u) x = 0x7E007E00u;
+        else e = max(e, es);
+        s_pair[wave][lane * NG + j] = x;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      auto read_pairs = [&](int at, uint32_t (&out)[8][NG]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NG; ++j) {
+            const v4u v = *reinterpret_cast<const v4u*>(&s_pair[wave][(at + 16 * h + 4 * g) * NG + 4 * j]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) out[4 * h + (4 * j + x) / NG][(4 * j + x) % NG] = v[x];
+          }
+      };
+      uint32_t kp[8][NG], vp[8][NG];
+      read_pairs(0, kp);
+      read_pairs(kTile, vp);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+
+      float x[8], most = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float y = 0.f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const half2v so = as_half2(kp[j][n]);
+          y += (float)so[1] * qsum[n];
+          y += (float)so[0] * s[n][j >> 2][j & 3];
+        }
+        x[j] = y * sc;
+      }
+      const int tile_first = first + i * kUnit;
+      if (!t.whole || __any(tile_first + kTile > length)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int tok = tile_first + (j >> 2) * 16 + 4 * g + (j & 3);
+          const bool on = ((t.live >> j) & 1) && tok < length;
+          x[j] = on ? x[j] : -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NG; ++n) vp[j][n] = on ? vp[j][n] : 0;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const bool grows = __any(lane >= kTile && e > largest);
+      if (grows) {
+        if (lane < kTile) e = 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) e = max(e, (uint32_t)__shfl_xor((int)e, d));
+        largest = max(largest, e);
+        E = (float)(int)(largest >> 10) - 14.f;
+      }
+      if (grows || __any(most > top)) {
+        top = fmaxf(top, most);
+        const float up = top + E;
+        const float shrink = up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up);
+        base = up;
+        sum *= shrink;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) osum[n] *= shrink;
+#pragma unroll
+        for (int n = 0; n < kAccs; ++n) acc[n] *= shrink;
+      }
+      const float ref = base == -INFINITY ? 0.f : base - 15.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j] - ref);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += x[j];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        v4u ph, pl;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const half2v a0 = as_half2(vp[2 * w][n]), a1 = as_half2(vp[2 * w + 1][n]);
+          osum[n] += x[2 * w] * (float)a0[1];
+          osum[n] += x[2 * w + 1] * (float)a1[1];
+          const float w0 = x[2 * w] * (float)a0[0], w1 = x[2 * w + 1] * (float)a1[0];
+          const auto h = __builtin_amdgcn_cvt_pkrtz(w0, w1);
+          ph[w] = __builtin_bit_cast(uint32_t, h);
+          pl[w] = pack_rtz(w0 - (float)h[0], w1 - (float)h[1]);
+        }
+#pragma unroll
+        for (int k = n * kAccs / NG; k < (n + 1) * kAccs / NG; ++k) {
+          const half8 v = R::values(t.v, k);
+          acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(ph), acc[k], 0, 0, 0);
+          acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(pl), acc[k], 0, 0, 0);
+        }
+      }
+    };
+
+    Tile even, odd;
+    if (tiles > 0) {
+      look_up(0);
+      request(even, 1);
+    }
+    for (int i = 0; i < tiles; i += 2) {
+      if (i + 1 < tiles) request(odd, i + 2);
+      compute(even, i);
+      if (i + 1 < tiles) {
+        if (i + 2 < tiles) request(even, i + 3);
+        compute(odd, i + 1);
+      }
+    }
+
+    // Join the four waves.
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      osum[n] += __shfl_xor(osum[n], 16);
+      osum[n] += __shfl_xor(osum[n], 32);
+    }
+    if (g == 0) s_ml[wave][m] = make_float2(base, sum);
+    if (m < columns) {
+#pragma unroll
+      for (int i = 0; i < kAccs; ++i)
+        *reinterpret_cast<floatx4*>(&s_acc[wave][m][i * 16 + g * 4]) =
+            acc[i] * (BITS == 4 && i % 2 ? 0x1p20f : 0x1p24f) + osum[i * NG / kAccs];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < columns * (D / 4); e += kThreads) {
+      const int h = e / (D / 4), d = e % (D / 4) * 4;
+      float mx = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_ml[w][h].x);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(s_ml[w][h].x - ref);
+        total += f * s_ml[w][h].y;
+        o += f * *reinterpret_cast<const floatx4*>(&s_acc[w][h][d]);
+      }
+      if (whole) {
+        T* out = static_cast<T*>(a.out) + (int64_t)(first_query + h / heads) * a.out_stride +
+                 (int64_t)(head0 + h % heads) * D + d;
+        store4(out, o * (total == 0.f ? 0.f : 1.f / total));
+      } else {
+        const int64_t at =
+            ((int64_t)(2 * blockIdx.y + (starts_run ? 0 : 1)) * gridDim.x + blockIdx.x) * 16 + h;
+        *reinterpret_cast<floatx4*>(p.acc + at * D + d) = o;
+        if (d == 0) p.ml[at] = make_float2(mx, total);
+      }
+    }
+    __syncthreads();  // s_ml and s_acc have been read
+  }
+}
+
+// Joins the pieces of one query and head, and writes zeros for queries without any.
+// Every wave forms the maximum and the sum itself; groups of D/4 lanes take the pieces
+// in turn.
+template <int D, bool WIDE>
+__global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args p) {
+  using T = std::conditional_t<WIDE, float, __half>;
+  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
+  __shared__ __align__(16) floatx4 s_part[kGroups][kLanes];
+  const seedlm_qcache_attend_args& a = p.a;
+  const int query = blockIdx.y, head = blockIdx.x;
+  int b = query;  // the item's first query
+  while (!starts_item(p, b)) --b;
+  const int units = p.ends[a.queries - 1], slots = min(p.slots, units);
+  const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
+  // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
+  // but the first they start the slot's run.
+  int first_slot = 0, pieces = 0, skip = 0;
+  if (u1 > u0) {
+    first_slot = slot_of(u0, units, slots);
+    pieces = slot_of(u1 - 1, units, slots) - first_slot + 1;
+    skip = slot_begin(first_slot, units, slots) != u0;
+  }
+  if (pieces == 1) return;
+  T* out = static_cast<T*>(a.out) + (int64_t)query * a.out_stride + (int64_t)head * D;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int in_group = head % p.group, heads = min(16, p.group - in_group / 16 * 16);
+  const int block = head / p.group * p.qtiles + in_group / 16;
+  const int column = (query - b) * heads + in_group % 16;
+  const int blocks = a.cache.kv_heads * p.qtiles;
+  auto partial = [&](int s) {
+    return ((int64_t)(2 * (first_slot + s) + (s == 0 ? skip : 0)) * blocks + block) * 16 + column;
+  };
+  float top = -INFINITY, total = 0.f;
+  for (int s = threadIdx.x & 63; s < pieces; s += 64) top = fmaxf(top, p.ml[partial(s)].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float ref = top == -INFINITY ? 0.f : top;
+  for (int s = threadIdx.x & 63; s < pieces; s += 64) {
+    const float2 ml = p.ml[partial(s)];
+    total += __builtin_amdgcn_exp2f(ml.x - ref) * ml.y;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = group; s < pieces; s += kGroups) {
+    const int64_t i = partial(s);
+    const float f = __builtin_amdgcn_exp2f(p.ml[i].x - ref);
+    o += f * *reinterpret_cast<const floatx4*>(p.acc + i * D + lane * 4);
+  }
+  s_part[group][lane] = o;
+  __syncthreads();
+  if (group != 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) o += s_part[k][lane];
+  store4(out + lane * 4, o * (total == 0.f ? 0.f : 1.f / total));
+}
+
+template <int D, int BITS, int NG, bool WIDE>
+int run_groups(const Args& p, hipStream_t s) {
+  const seedlm_qcache_attend_args& a = p.a;
+  const bool split = p.slots > 0;
+  hipLaunchKernelGGL((qcache_attend_kernel<D, BITS, NG, WIDE>),
+                     dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries), dim3(kThreads),
+                     split ? a.queries * sizeof(int32_t) : 0, s, p);
+  if (split)
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE>), dim3(a.heads, a.queries),
+                       dim3(kThreads), 0, s, p);
+  return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
+}
+
+// A checked call of one code width and one type of queries; each is a source of its own.
+template <int BITS, bool WIDE>
+int run(const Args& p, hipStream_t s) {
+  const int groups = p.a.cache.head_dim / p.a.cache.group;
+  switch (p.a.cache.head_dim) {
+    case 64: return groups == 1 ? run_groups<64, BITS, 1, WIDE>(p, s)
+                                : run_groups<64, BITS, 2, WIDE>(p, s);
+    case 128: return groups == 1 ? run_groups<128, BITS, 1, WIDE>(p, s)
+                   : groups == 2 ? run_groups<128, BITS, 2, WIDE>(p, s)
+                                 : run_groups<128, BITS, 4, WIDE>(p, s);
+    case 256: return groups == 1 ? run_groups<256, BITS, 1, WIDE>(p, s)
+                   : groups == 2 ? run_groups<256, BITS, 2, WIDE>(p, s)
+                                 : run_groups<256, BITS, 4, WIDE>(p, s);
+    default: return SEEDLM_E_UNSUPPORTED;
+  }
+}
+int run_4(const Args& p, hipStream_t s);
+int run_4_wide(const Args& p, hipStream_t s);
+int run_8(const Args& p, hipStream_t s);
+int run_8_wide(const Args& p, hipStream_t s);
+
+}  // namespace qattend
+}  // namespace seedlm
