@@ -1,7 +1,8 @@
 // What the attention kernels share: how the work of requests of any lengths is cut
-// into even runs of units, and page numbers without a division.
+// into even runs of units.
 #pragma once
 
+#include "divisor.h"
 #include "seedlm_internal.h"
 
 namespace seedlm {
@@ -51,20 +52,6 @@ __device__ inline int request_of(const int32_t* ends, int n, int u) {
     else lo = mid + 1;
   }
   return lo;
-}
-
-// x / d for 0 <= x < 2^31, with 2^(L-1) < d <= 2^L: ceil(2^(31+L) / d) is less
-// than 1 above 2^(31+L) / d, so the product is less than x / 2^(31+L) < 2^-L
-// above x / d.  That is at most 1/d, which no quotient's fraction lacks less
-// than to the next whole number, so the floor is the quotient's.
-struct Divisor {
-  uint32_t mul, shift;
-  __device__ uint32_t of(uint32_t x) const { return (uint32_t)(((uint64_t)x * mul) >> shift); }
-};
-inline Divisor divisor(uint32_t d) {
-  uint32_t L = 0;
-  while (((uint64_t)1 << L) < d) ++L;
-  return {(uint32_t)((((uint64_t)1 << (31 + L)) + d - 1) / d), 31 + L};
 }
 
 }  // namespace seedlm

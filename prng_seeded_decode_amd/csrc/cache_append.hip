@@ -16,50 +16,12 @@
 // 2048 tokens of 32 and 8 heads, fp32 (93 MB), in 18.2 us, 5.1 TB/s, and fp16 with 120
 // of the 128 dimensions rotated, so by units of one pair (51 MB), in 24.6 us, 2.1 TB/s:
 // their 2-byte accesses take 16 times the instructions.
-#include <hip/hip_fp16.h>
-
-#include "seedlm_internal.h"
+#include "rotary.h"
 
 namespace seedlm {
 namespace {
 
 constexpr int kThreads = 256;
-
-// N elements at p as fp32, and back; N * sizeof(T) bytes, aligned to 16 where
-// that is a multiple of 16.
-template <int N, typename T>
-__device__ void load(const T* p, float (&v)[N]) {
-  if constexpr (N == 8 && sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const __half* h = reinterpret_cast<const __half*>(&u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __half2float(h[i]);
-  } else if constexpr (N == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    static_assert(N == 1, "");
-    v[0] = (float)p[0];
-  }
-}
-
-template <int N, typename T>
-__device__ void store(T* p, const float (&v)[N]) {
-  if constexpr (N == 8 && sizeof(T) == 2) {
-    uint4 u;
-    __half* h = reinterpret_cast<__half*>(&u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __float2half_rn(v[i]);
-    *reinterpret_cast<uint4*>(p) = u;
-  } else if constexpr (N == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    p[0] = (T)v[0];
-  }
-}
 
 struct AppendArgs {
   seedlm_cache_append_args a;
@@ -84,14 +46,9 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(const AppendArgs
     cache_at = page * a.cache.page_stride +
                (slot - page * a.cache.page_size) * a.cache.token_stride;
   }
-  // The unit's two runs of N elements: the halves of N rotated pairs, or (as
-  // interleaved pairs and unrotated elements are) 2N in a row.
-  const int e0 = unit * 2 * N;
-  const bool rotated = e0 < a.rot;
-  const bool split = rotated && !a.interleaved;
-  const int lo = split ? unit * N : e0, hi = split ? lo + a.rot / 2 : e0 + N;
+  const RotaryUnit<N> u(unit, a.rot, a.interleaved);
   float c[N], s[N];
-  if (rotated && turns) {
+  if (u.rotated && turns) {
     const int64_t at = (int64_t)pos * (a.rot / 2) + unit * N;
     load<N>(a.cos + at, c);
     load<N>(a.sin + at, s);
@@ -105,48 +62,24 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(const AppendArgs
                       : (is_v ? static_cast<const T*>(a.v) + t * a.v_stride + hk * D
                               : static_cast<const T*>(a.k) + t * a.k_stride + hk * D);
   float x[N], y[N];
-  load<N>(src + lo, x);
-  load<N>(src + hi, y);
-  if (rotated && !is_v && turns) {
-    if (split) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float u = x[i], w = y[i];
-        x[i] = u * c[i] - w * s[i];
-        y[i] = w * c[i] + u * s[i];
-      }
-    } else {
-      // elements 2i, 2i + 1 of the 2N in a row
-      float z[2 * N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = x[i], z[N + i] = y[i];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float u = z[2 * i], w = z[2 * i + 1];
-        z[2 * i] = u * c[i] - w * s[i];
-        z[2 * i + 1] = w * c[i] + u * s[i];
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = z[i], y[i] = z[N + i];
-    }
-  }
+  load<N>(src + u.lo, x);
+  load<N>(src + u.hi, y);
+  if (u.rotated && !is_v && turns) u.turn(x, y, c, s);
   if (is_q) {
     T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * D;
     if (!turns) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = y[i] = 0.f;
     }
-    store<N>(dst + lo, x);
-    store<N>(dst + hi, y);
+    store<N>(dst + u.lo, x);
+    store<N>(dst + u.hi, y);
   } else {
     __half* dst = static_cast<__half*>(is_v ? a.cache.v : a.cache.k) + cache_at +
                   hk * a.cache.head_stride;
-    store<N>(dst + lo, x);
-    store<N>(dst + hi, y);
+    store<N>(dst + u.lo, x);
+    store<N>(dst + u.hi, y);
   }
 }
-
-bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 // Whether every access of the 8-pair units is aligned to 16 bytes.
 bool wide_units(const seedlm_cache_append_args& a) {

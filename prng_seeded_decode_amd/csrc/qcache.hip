@@ -3,129 +3,402 @@
 //
 // A group of x of a row gets offset o = min x, scale s = fp16((max x - o) / levels) and
 // codes c = rint((x - o) / s); it reads back as o + s c.  The x are fp16 numbers, so o
-// is exact.  Each element is read and written once, so memory bandwidth bounds both.
-#include <hip/hip_fp16.h>
+// is exact.  Each element is read and written once with some 20 operations, so memory
+// bandwidth bounds both.
+//
+// Four lanes take a row, four units each: for every i elements 16i + 4u .. 16i + 4u + 3
+// of lane u, one load of 8 or 16 bytes.  A lane then has whole units of codes, which it
+// packs in registers, and a group's extremes are its own over some i and two exchanges
+// with its neighbours.  The other half of a rotated pair is loaded too (it is in the
+// caches) and not exchanged, so that any part of a head may turn.  q goes through the
+// units of rotary.h in workgroups of its own.
+#include <type_traits>
 
-#include "seedlm_internal.h"
+#include "divisor.h"
+#include "rotary.h"
 
 namespace seedlm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRows = kThreads / 4;  // rows of a workgroup
 
-// Element d of a row: its unit, its place in the unit.
-__device__ int byte_of(int d, int dim, int bits) { return ((d % 16) * (dim / 16) + d / 16) * bits / 8; }
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-// Element e of a head at `x` turned by a token's cosines and sines, each operation
-// rounded: codes next to a border must not depend on how the compiler joins them.
-template <typename T>
-__device__ float turned(const T* x, int e, int rot, bool interleaved, const float* cos,
-                        const float* sin) {
+// Four elements at p as fp32; VEC: aligned to their size.
+template <bool VEC, typename T>
+__device__ void load4(const T* p, float (&v)[4]) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    const v2u u = *reinterpret_cast<const v2u*>(p);
+    const __half* h = reinterpret_cast<const __half*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __half2float(h[i]);
+  } else if constexpr (VEC) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)p[i];
+  }
+}
+
+template <bool VEC, typename T>
+__device__ void store4(T* p, const float (&v)[4]) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    v2u u;
+    __half* h = reinterpret_cast<__half*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float2half_rn(v[i]);
+    *reinterpret_cast<v2u*>(p) = u;
+  } else if constexpr (VEC) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = (T)v[i];
+  }
+}
+
+// Elements e .. e + 3 of the head at `x`, turned by a token's cosines and sines.  Each
+// operation is rounded: codes next to a border must not depend on how the compiler
+// joins them.  VEC: pairs and angles lie in aligned fours.
+template <bool VEC, typename T>
+__device__ void turned4(const T* x, int e, int rot, bool interleaved, const float* cos,
+                        const float* sin, float (&y)[4]) {
 #pragma clang fp contract(off)
-  if (e >= rot) return (float)x[e];
   const int half = rot / 2;
-  const int pair = interleaved ? e / 2 : e % half;
-  const bool second = interleaved ? e % 2 : e >= half;
-  const float a = (float)x[interleaved ? 2 * pair : pair];
-  const float b = (float)x[interleaved ? 2 * pair + 1 : pair + half];
-  const float c = cos[pair], s = sin[pair];
-  return second ? b * c + a * s : a * c - b * s;
+  if constexpr (VEC) {
+    load4<true>(x + e, y);
+    if (e >= rot) return;
+    if (interleaved) {
+      const float2 c = *reinterpret_cast<const float2*>(cos + e / 2);
+      const float2 s = *reinterpret_cast<const float2*>(sin + e / 2);
+      const float a0 = y[0], b0 = y[1], a1 = y[2], b1 = y[3];
+      y[0] = a0 * c.x - b0 * s.x, y[1] = b0 * c.x + a0 * s.x;
+      y[2] = a1 * c.y - b1 * s.y, y[3] = b1 * c.y + a1 * s.y;
+    } else {
+      const bool second = e >= half;
+      float o[4], c[4], s[4];
+      load4<true>(x + (second ? e - half : e + half), o);
+      load4<true>(cos + (second ? e - half : e), c);
+      load4<true>(sin + (second ? e - half : e), s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = y[j] * c[j], w = o[j] * s[j];
+        y[j] = second ? u + w : u - w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j, ++e) {
+      if (e >= rot) {
+        y[j] = (float)x[e];
+        continue;
+      }
+      const int pair = interleaved ? e / 2 : e % half;
+      const bool second = interleaved ? e % 2 : e >= half;
+      const float a = (float)x[interleaved ? 2 * pair : pair];
+      const float b = (float)x[interleaved ? 2 * pair + 1 : pair + half];
+      const float c = cos[pair], s = sin[pair];
+      y[j] = second ? b * c + a * s : a * c - b * s;
+    }
+  }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void qcache_append_kernel(const seedlm_qcache_append_args a) {
-  const int64_t t = blockIdx.x;
+// f over the four lanes of a row.
+template <typename F>
+__device__ float over_row(float x, F f) {
+  auto swap = [](float v, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                                 decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  x = f(x, swap(x, std::integral_constant<int, 0xB1>()));  // lanes 1, 0, 3, 2
+  return f(x, swap(x, std::integral_constant<int, 0x4E>()));  // lanes 2, 3, 0, 1
+}
+
+// N dwords at p, aligned to their size up to 16 bytes.
+template <int N>
+__device__ void load_dwords(const void* p, uint32_t (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = *static_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const v2u u = *static_cast<const v2u*>(p);
+    v[0] = u[0], v[1] = u[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const v4u u = static_cast<const v4u*>(p)[i / 4];
+      v[i] = u[0], v[i + 1] = u[1], v[i + 2] = u[2], v[i + 3] = u[3];
+    }
+  }
+}
+template <int N>
+__device__ void store_dwords(void* p, const uint32_t (&v)[N]) {
+  if constexpr (N == 1) {
+    *static_cast<uint32_t*>(p) = v[0];
+  } else if constexpr (N == 2) {
+    *static_cast<v2u*>(p) = v2u{v[0], v[1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) static_cast<v4u*>(p)[i / 4] = v4u{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  }
+}
+
+// Where a slot's row of a head lies: byte of its codes, number of its first pair.
+struct RowAt {
+  int64_t codes, pair;
+  __device__ RowAt(const seedlm_qcache_t& c, int slot, int head) {
+    const int page = slot / c.page_size, nth = slot - page * c.page_size;
+    codes = page * c.page_stride + nth * c.token_stride + head * c.head_stride;
+    pair = page * c.scale_page_stride + nth * c.scale_token_stride + head * c.scale_head_stride;
+  }
+};
+
+// Rows of k and v lie token after token, a token's keys before its values; a workgroup
+// takes whole tokens, or 64 rows of one.
+struct RowSplit {
+  int tokens;  // of a workgroup
+  int passes;  // workgroups of a token
+  Divisor rows;  // of a token
+  explicit RowSplit(int kv_heads) {
+    tokens = 2 * kv_heads < kRows ? kRows / (2 * kv_heads) : 1;
+    passes = (2 * kv_heads + kRows - 1) / kRows;
+    rows = divisor((uint32_t)(2 * kv_heads));
+  }
+  // The token (counted in the workgroup) and the row of it that thread row `r` of pass
+  // `pass` takes; false for none.
+  __device__ bool at(int r, int pass, int kv_heads, int* token, int* row) const {
+    *token = passes > 1 ? 0 : (int)rows.of(r);
+    *row = passes > 1 ? pass * kRows + r : r - *token * 2 * kv_heads;
+    return *token < tokens && *row < 2 * kv_heads;
+  }
+};
+
+struct AppendArgs {
+  seedlm_qcache_append_args a;
+  RowSplit split;
+  int units;            // units of a head of q
+  Divisor token_units;  // units of a token of q
+};
+
+// VEC: k, v and the angles in aligned fours.  N: pairs of a unit of q, 8 or 1.
+template <int D, int BITS, int NG, bool VEC, int N, typename T>
+__global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArgs p) {
+  const seedlm_qcache_append_args& a = p.a;
   const seedlm_qcache_t& c = a.cache;
-  const int D = c.head_dim, groups = D / c.group;
+  const int64_t t0 = (int64_t)blockIdx.x * p.split.tokens;
+  if ((int)blockIdx.y >= p.split.passes) {  // q
+    const int i = (blockIdx.y - p.split.passes) * kThreads + threadIdx.x;
+    const int token = (int)p.token_units.of(i);
+    const int64_t t = t0 + token;
+    if (token >= p.split.tokens || t >= a.tokens) return;
+    const int j = i - token * p.units * a.heads, h = j / p.units;
+    const RotaryUnit<N> u(j - h * p.units, a.rot, a.interleaved);
+    const int pos = a.positions[t];
+    const bool turns = pos >= 0 && pos < a.table_len;
+    const T* src = static_cast<const T*>(a.q) + t * a.q_stride + (int64_t)h * D;
+    T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + (int64_t)h * D;
+    float x[N], y[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = y[k] = 0.f;
+    if (turns) {
+      load<N>(src + u.lo, x);
+      load<N>(src + u.hi, y);
+      if (u.rotated) {
+        float co[N], si[N];
+        const int64_t at = (int64_t)pos * (a.rot / 2) + (j - h * p.units) * N;
+        load<N>(a.cos + at, co);
+        load<N>(a.sin + at, si);
+        u.turn(x, y, co, si);
+      }
+    }
+    store<N>(dst + u.lo, x);
+    store<N>(dst + u.hi, y);
+    return;
+  }
+  constexpr int kI = D / 16;                 // codes of a unit
+  constexpr int kUnitBytes = kI * BITS / 8;
+  constexpr int KD = kUnitBytes;             // dwords of 4 units
+  constexpr float kLevels = (1 << BITS) - 1;
+  const int u = threadIdx.x & 3;
+  int token, row;
+  if (!p.split.at(threadIdx.x >> 2, blockIdx.y, c.kv_heads, &token, &row)) return;
+  const int64_t t = t0 + token;
+  if (t >= a.tokens) return;
   const int pos = a.positions[t], slot = a.slots[t];
-  const bool turns = pos >= 0 && pos < a.table_len;
-  const float* cos = a.cos + (turns ? (int64_t)pos * (a.rot / 2) : 0);
-  const float* sin = a.sin + (turns ? (int64_t)pos * (a.rot / 2) : 0);
-  // every thread keeps its head's unrotated elements until all have been read (q_out
-  // may be q), so a head is a workgroup's turn
-  for (int h = 0; h < a.heads; ++h) {
-    const T* q = static_cast<const T*>(a.q) + t * a.q_stride + (int64_t)h * D;
-    T* out = static_cast<T*>(a.q_out) + t * a.q_out_stride + (int64_t)h * D;
-    const int e = threadIdx.x;
-    float x = 0.f;
-    if (e < D && turns) x = turned(q, e, a.rot, a.interleaved, cos, sin);
-    __syncthreads();
-    if (e < D) out[e] = (T)x;
-  }
-  if (!turns || slot < 0 || slot >= c.pages * c.page_size) return;
-  const int page = slot / c.page_size, nth = slot % c.page_size;
-  const float levels = (float)((1 << c.bits) - 1);
-  for (int i = threadIdx.x; i < 2 * c.kv_heads * groups; i += kThreads) {
-    const int g = i % groups, h = i / groups % c.kv_heads;
-    const bool is_v = i >= c.kv_heads * groups;
-    const T* src = (is_v ? static_cast<const T*>(a.v) + t * a.v_stride
-                         : static_cast<const T*>(a.k) + t * a.k_stride) + (int64_t)h * D;
-    const int rot = is_v ? 0 : a.rot;
-    auto value = [&](int e) { return (float)(_Float16)turned(src, e, rot, a.interleaved, cos, sin); };
-    float low = INFINITY, high = -INFINITY, sum = 0.f;
-    for (int e = g * c.group; e < (g + 1) * c.group; ++e) {
-      const float x = value(e);
-      low = fminf(low, x), high = fmaxf(high, x), sum += x * 0.f;
-    }
-    const bool finite = sum == 0.f;
-    const _Float16 scale = finite ? (_Float16)((high - low) / levels) : (_Float16)NAN;
+  if (pos < 0 || pos >= a.table_len || slot < 0 || slot >= c.pages * c.page_size) return;
+  const bool is_v = row >= c.kv_heads;
+  const int h = is_v ? row - c.kv_heads : row;
+  const T* src = (is_v ? static_cast<const T*>(a.v) + t * a.v_stride
+                       : static_cast<const T*>(a.k) + t * a.k_stride) + (int64_t)h * D;
+  const int rot = is_v ? 0 : a.rot;
+  const int64_t angle = (int64_t)pos * (a.rot / 2);
+  float x[kI][4];
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+    turned4<VEC>(src, 16 * i + 4 * u, rot, a.interleaved, a.cos + angle, a.sin + angle, x[i]);
+
+  uint32_t even[KD], odd[KD], pair[NG];  // bytes of codes of even and of odd i
+#pragma unroll
+  for (int k = 0; k < KD; ++k) even[k] = odd[k] = 0;
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    float low = INFINITY, high = -INFINITY, finite = 0.f;
+#pragma unroll
+    for (int i = n * kI / NG; i < (n + 1) * kI / NG; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[i][j] = (float)(_Float16)x[i][j];
+        low = fminf(low, x[i][j]), high = fmaxf(high, x[i][j]);
+        finite += x[i][j] * 0.f;  // NaN from the first NaN or infinity on
+      }
+    low = over_row(low, [](float v, float w) { return fminf(v, w); });
+    high = over_row(high, [](float v, float w) { return fmaxf(v, w); });
+    finite = over_row(finite, [](float v, float w) { return v + w; });
+    const _Float16 scale = (_Float16)((high - low) / kLevels);
     const float s = (float)scale;
-    auto code = [&](int e) -> uint32_t {
-      return finite && s > 0.f ? (uint32_t)fminf(rintf((value(e) - low) / s), levels) : 0;
-    };
-    uint8_t* row = static_cast<uint8_t*>(is_v ? c.v : c.k) + page * c.page_stride +
-                   nth * c.token_stride + h * c.head_stride;
-    for (int e = g * c.group; e < (g + 1) * c.group; ++e) {
-      if (c.bits == 8) row[byte_of(e, D, 8)] = (uint8_t)code(e);
-      else if (e / 16 % 2 == 0) row[byte_of(e, D, 4)] = (uint8_t)(code(e) | code(e + 16) << 4);
+    const bool codes = finite == 0.f && s > 0.f;
+#pragma unroll
+    for (int i = n * kI / NG; i < (n + 1) * kI / NG; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float code = codes ? fminf(rintf((x[i][j] - low) / s), kLevels) : 0.f;
+        const int byte = j * kUnitBytes + i * BITS / 8;
+        uint32_t& d = BITS == 4 && i % 2 ? odd[byte / 4] : even[byte / 4];
+        d = __builtin_amdgcn_cvt_pk_u8_f32(code, byte % 4, d);
+      }
+    const uint32_t lo = __builtin_bit_cast(uint16_t, scale);
+    const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)low);
+    pair[n] = finite == 0.f ? lo | hi << 16 : 0x7E00u;
+  }
+#pragma unroll
+  for (int k = 0; k < KD; ++k) even[k] |= odd[k] << 4;
+  const RowAt at(c, slot, h);
+  store_dwords(static_cast<uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, even);
+  if (u == 0) store_dwords(static_cast<uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
+}
+
+struct ReadArgs {
+  seedlm_qcache_read_args a;
+  RowSplit split;
+};
+
+// VEC: rows of the outputs in aligned fours.
+template <int D, int BITS, int NG, bool VEC, typename T>
+__global__ __launch_bounds__(kThreads) void qcache_read_kernel(const ReadArgs p) {
+  constexpr int kI = D / 16, kUnitBytes = kI * BITS / 8, KD = kUnitBytes;
+  const seedlm_qcache_read_args& a = p.a;
+  const seedlm_qcache_t& c = a.cache;
+  const int u = threadIdx.x & 3;
+  int token, row;
+  if (!p.split.at(threadIdx.x >> 2, blockIdx.y, c.kv_heads, &token, &row)) return;
+  const int64_t t = (int64_t)blockIdx.x * p.split.tokens + token;
+  if (t >= a.tokens) return;
+  const bool is_v = row >= c.kv_heads;
+  if (!(is_v ? a.v_out : a.k_out)) return;
+  const int h = is_v ? row - c.kv_heads : row, slot = a.slots[t];
+  uint32_t code[KD], pair[NG];
+#pragma unroll
+  for (int k = 0; k < KD; ++k) code[k] = 0;
+#pragma unroll
+  for (int n = 0; n < NG; ++n) pair[n] = 0;
+  if (slot >= 0 && slot < c.pages * c.page_size) {
+    const RowAt at(c, slot, h);
+    load_dwords(static_cast<const uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, code);
+    load_dwords(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
+  }
+  T* out = (is_v ? static_cast<T*>(a.v_out) + t * a.v_stride
+                 : static_cast<T*>(a.k_out) + t * a.k_stride) + (int64_t)h * D + 4 * u;
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const uint32_t so = pair[i * NG / kI];
+    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)so);
+    const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)(so >> 16));
+    float x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int byte = j * kUnitBytes + i * BITS / 8;
+      uint32_t d = code[byte / 4];
+      if (BITS == 4) d = (i % 2 ? d >> 4 : d) & 0x0F0F0F0Fu;
+      x[j] = o + s * (float)(d >> (8 * (byte % 4)) & 0xFF);
     }
-    _Float16* pair = static_cast<_Float16*>(is_v ? c.v_scale : c.k_scale) +
-                     2 * (page * c.scale_page_stride + nth * c.scale_token_stride +
-                          h * c.scale_head_stride + g);
-    pair[0] = scale;
-    pair[1] = finite ? (_Float16)low : (_Float16)0.f;
+    store4<VEC>(out + 16 * i, x);
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void qcache_read_kernel(const seedlm_qcache_read_args a) {
-  const int64_t t = blockIdx.x;
-  const seedlm_qcache_t& c = a.cache;
-  const int D = c.head_dim, slot = a.slots[t];
-  const bool live = slot >= 0 && slot < c.pages * c.page_size;
-  const int page = live ? slot / c.page_size : 0, nth = live ? slot % c.page_size : 0;
-  for (int i = threadIdx.x; i < 2 * c.kv_heads * D; i += kThreads) {
-    const int e = i % D, h = i / D % c.kv_heads;
-    const bool is_v = i >= c.kv_heads * D;
-    T* out = static_cast<T*>(is_v ? a.v_out : a.k_out);
-    if (!out) continue;
-    float x = 0.f;
-    if (live) {
-      const uint8_t* row = static_cast<const uint8_t*>(is_v ? c.v : c.k) + page * c.page_stride +
-                           nth * c.token_stride + h * c.head_stride;
-      const _Float16* pair = static_cast<const _Float16*>(is_v ? c.v_scale : c.k_scale) +
-                             2 * (page * c.scale_page_stride + nth * c.scale_token_stride +
-                                  h * c.scale_head_stride + e / c.group);
-      const uint32_t byte = row[byte_of(e, D, c.bits)];
-      const uint32_t code = c.bits == 8 ? byte : byte >> (e / 16 % 2 * 4) & 15;
-      x = (float)pair[1] + (float)pair[0] * (float)code;
-    }
-    out[t * (is_v ? a.v_stride : a.k_stride) + (int64_t)h * D + e] = (T)x;
-  }
+bool fours(const void* p, int64_t stride, int dtype) {
+  return stride % 4 == 0 && (uintptr_t)p % (dtype == SEEDLM_F16 ? 8 : 16) == 0;
 }
+
+// Whether q's rows and angles can go by units of 8 pairs.
+bool wide_units(const seedlm_qcache_append_args& a) {
+  const int64_t per = a.x_dtype == SEEDLM_F16 ? 8 : 4;  // elements of 16 bytes
+  return a.rot % 16 == 0 && a.q_stride % per == 0 && a.q_out_stride % per == 0 && aligned16(a.q) &&
+         aligned16(a.q_out) && aligned16(a.cos) && aligned16(a.sin);
+}
+
+// f with the cache's row as compile-time numbers: f(D, BITS, NG).
+template <typename F>
+int with_row(const seedlm_qcache_t& c, F f) {
+  auto groups = [&](auto d, auto bits) {
+    const int n = c.head_dim / c.group;
+    if (n == 1) return f(d, bits, std::integral_constant<int, 1>());
+    if (n == 2) return f(d, bits, std::integral_constant<int, 2>());
+    if constexpr (decltype(d)::value > 64) return f(d, bits, std::integral_constant<int, 4>());
+    return (int)SEEDLM_E_UNSUPPORTED;
+  };
+  auto width = [&](auto d) {
+    return c.bits == 4 ? groups(d, std::integral_constant<int, 4>())
+                       : groups(d, std::integral_constant<int, 8>());
+  };
+  if (c.head_dim == 64) return width(std::integral_constant<int, 64>());
+  if (c.head_dim == 128) return width(std::integral_constant<int, 128>());
+  return width(std::integral_constant<int, 256>());
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE; }
 
 }  // namespace
 
 int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
-  const auto kernel = a.x_dtype == SEEDLM_F16 ? qcache_append_kernel<__half> : qcache_append_kernel<float>;
-  hipLaunchKernelGGL(kernel, dim3(a.tokens), dim3(kThreads), 0, s, a);
-  return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
+  const int D = a.cache.head_dim;
+  const bool vec = fours(a.k, a.k_stride, a.x_dtype) && fours(a.v, a.v_stride, a.x_dtype) &&
+                   a.rot % 8 == 0 && aligned16(a.cos) && aligned16(a.sin);
+  const bool wide = vec && wide_units(a);
+  AppendArgs p{a, RowSplit(a.cache.kv_heads), wide ? D / 16 : D / 2, {}};
+  if (a.heads > 1024) p.split.tokens = 1;  // the grid's second dimension is short
+  const int token_units = a.heads * p.units;
+  p.token_units = divisor((uint32_t)token_units);
+  const int q_passes = (p.split.tokens * token_units + kThreads - 1) / kThreads;
+  const dim3 grid((a.tokens + p.split.tokens - 1) / p.split.tokens, p.split.passes + q_passes);
+  return with_row(a.cache, [&](auto d, auto bits, auto groups) {
+    constexpr int kD = decltype(d)::value, kBits = decltype(bits)::value, kG = decltype(groups)::value;
+    const bool f16 = a.x_dtype == SEEDLM_F16;
+    const auto kernel =
+        wide ? (f16 ? qcache_append_kernel<kD, kBits, kG, true, 8, __half>
+                    : qcache_append_kernel<kD, kBits, kG, true, 8, float>)
+             : (f16 ? qcache_append_kernel<kD, kBits, kG, false, 1, __half>
+                    : qcache_append_kernel<kD, kBits, kG, false, 1, float>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, p);
+    return launched();
+  });
 }
 
 int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s) {
-  const auto kernel = a.y_dtype == SEEDLM_F16 ? qcache_read_kernel<__half> : qcache_read_kernel<float>;
-  hipLaunchKernelGGL(kernel, dim3(a.tokens), dim3(kThreads), 0, s, a);
-  return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
+  const ReadArgs p{a, RowSplit(a.cache.kv_heads)};
+  const bool vec = (!a.k_out || fours(a.k_out, a.k_stride, a.y_dtype)) &&
+                   (!a.v_out || fours(a.v_out, a.v_stride, a.y_dtype));
+  const dim3 grid((a.tokens + p.split.tokens - 1) / p.split.tokens, p.split.passes);
+  return with_row(a.cache, [&](auto d, auto bits, auto groups) {
+    constexpr int kD = decltype(d)::value, kBits = decltype(bits)::value, kG = decltype(groups)::value;
+    const bool f16 = a.y_dtype == SEEDLM_F16;
+    const auto kernel = vec ? (f16 ? qcache_read_kernel<kD, kBits, kG, true, __half>
+                                   : qcache_read_kernel<kD, kBits, kG, true, float>)
+                            : (f16 ? qcache_read_kernel<kD, kBits, kG, false, __half>
+                                   : qcache_read_kernel<kD, kBits, kG, false, float>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, p);
+    return launched();
+  });
 }
 
 }  // namespace seedlm
