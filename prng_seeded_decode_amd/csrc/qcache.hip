@@ -24,6 +24,7 @@ constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 4;  // rows of a workgroup
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 // Four elements at p as fp32; VEC: aligned to their size.
@@ -84,8 +85,8 @@ __device__ void turned4(const T* x, int e, int rot, bool interleaved, const floa
       load4<true>(sin + (second ? e - half : e), s);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float u = y[j] * c[j], w = o[j] * s[j];
-        y[j] = second ? u + w : u - w;
+        const float u = y[j] * c[j], w = o[j] * (second ? s[j] : -s[j]);
+        y[j] = u + w;
       }
     }
   } else {
@@ -105,16 +106,21 @@ __device__ void turned4(const T* x, int e, int rot, bool interleaved, const floa
   }
 }
 
-// f over the four lanes of a row.
-template <typename F>
-__device__ float over_row(float x, F f) {
-  auto swap = [](float v, auto ctrl) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
-                                                                 decltype(ctrl)::value, 0xF, 0xF, true));
-  };
-  x = f(x, swap(x, std::integral_constant<int, 0xB1>()));  // lanes 1, 0, 3, 2
-  return f(x, swap(x, std::integral_constant<int, 0x4E>()));  // lanes 2, 3, 0, 1
+// The value of another lane of the same four; CTRL: its place, two bits a lane.
+template <int CTRL>
+__device__ uint32_t in_row(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
+constexpr int kSwapOne = 0xB1, kSwapTwo = 0x4E;  // lanes 1, 0, 3, 2 and 2, 3, 0, 1
+
+// The least and the largest of both halves of x over the four lanes of a row; NaN if
+// there is one.
+__device__ float least(half2v x) {
+  float y = __builtin_elementwise_minimum((float)x[0], (float)x[1]);
+  y = __builtin_elementwise_minimum(y, __builtin_bit_cast(float, in_row<kSwapOne>(__builtin_bit_cast(uint32_t, y))));
+  return __builtin_elementwise_minimum(y, __builtin_bit_cast(float, in_row<kSwapTwo>(__builtin_bit_cast(uint32_t, y))));
+}
+__device__ float largest(half2v x) { return -least(-x); }
 
 // N dwords at p, aligned to their size up to 16 bytes.
 template <int N>
@@ -233,43 +239,63 @@ __global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArg
                        : static_cast<const T*>(a.k) + t * a.k_stride) + (int64_t)h * D;
   const int rot = is_v ? 0 : a.rot;
   const int64_t angle = (int64_t)pos * (a.rot / 2);
-  float x[kI][4];
+  half2v x[kI][2];
 #pragma unroll
-  for (int i = 0; i < kI; ++i)
-    turned4<VEC>(src, 16 * i + 4 * u, rot, a.interleaved, a.cos + angle, a.sin + angle, x[i]);
+  for (int i = 0; i < kI; ++i) {
+    float y[4];
+    turned4<VEC>(src, 16 * i + 4 * u, rot, a.interleaved, a.cos + angle, a.sin + angle, y);
+    x[i][0] = half2v{(_Float16)y[0], (_Float16)y[1]};
+    x[i][1] = half2v{(_Float16)y[2], (_Float16)y[3]};
+  }
 
   uint32_t even[KD], odd[KD], pair[NG];  // bytes of codes of even and of odd i
 #pragma unroll
   for (int k = 0; k < KD; ++k) even[k] = odd[k] = 0;
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
-    float low = INFINITY, high = -INFINITY, finite = 0.f;
+    constexpr int kN = kI / NG;
+    half2v lows = x[n * kN][0], highs = lows;
 #pragma unroll
-    for (int i = n * kI / NG; i < (n + 1) * kI / NG; ++i)
+    for (int i = n * kN; i < (n + 1) * kN; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[i][j] = (float)(_Float16)x[i][j];
-        low = fminf(low, x[i][j]), high = fmaxf(high, x[i][j]);
-        finite += x[i][j] * 0.f;  // NaN from the first NaN or infinity on
+      for (int j = 0; j < 2; ++j) {
+        lows = __builtin_elementwise_minimum(lows, x[i][j]);
+        highs = __builtin_elementwise_maximum(highs, x[i][j]);
       }
-    low = over_row(low, [](float v, float w) { return fminf(v, w); });
-    high = over_row(high, [](float v, float w) { return fmaxf(v, w); });
-    finite = over_row(finite, [](float v, float w) { return v + w; });
+    const float low = least(lows), high = largest(highs);
+    const bool finite = high - low < INFINITY;
     const _Float16 scale = (_Float16)((high - low) / kLevels);
     const float s = (float)scale;
-    const bool codes = finite == 0.f && s > 0.f;
+    // (x - o) / s by way of 1 / s is off by less than 2^-22 of itself, 2^-14 here, so it
+    // rounds to the same code but within that of the middle between two.  There, and
+    // where the last code might be passed, the wave divides.
+    const bool codes = finite && s > 0.f;
+    const float inverse = codes ? 1.f / s : 0.f;
+    const bool passes = (high - low) * inverse > kLevels + 0.25f;
 #pragma unroll
-    for (int i = n * kI / NG; i < (n + 1) * kI / NG; ++i)
+    for (int i = n * kN; i < (n + 1) * kN; ++i) {
+      float d[4], code[4], off = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float code = codes ? fminf(rintf((x[i][j] - low) / s), kLevels) : 0.f;
-        const int byte = j * kUnitBytes + i * BITS / 8;
-        uint32_t& d = BITS == 4 && i % 2 ? odd[byte / 4] : even[byte / 4];
-        d = __builtin_amdgcn_cvt_pk_u8_f32(code, byte % 4, d);
+        d[j] = (float)x[i][j / 2][j % 2] - low;
+        const float y = d[j] * inverse;
+        code[j] = rintf(y);
+        off = fmaxf(off, fabsf(y - code[j]));
       }
+      if (__any(passes || off > 0.5f - 0x1p-14f)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code[j] = codes ? fminf(rintf(d[j] / s), kLevels) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int byte = j * kUnitBytes + i * BITS / 8;
+        uint32_t& w = BITS == 4 && i % 2 ? odd[byte / 4] : even[byte / 4];
+        w = __builtin_amdgcn_cvt_pk_u8_f32(code[j], byte % 4, w);
+      }
+    }
     const uint32_t lo = __builtin_bit_cast(uint16_t, scale);
     const uint32_t hi = __builtin_bit_cast(uint16_t, (_Float16)low);
-    pair[n] = finite == 0.f ? lo | hi << 16 : 0x7E00u;
+    pair[n] = finite ? lo | hi << 16 : 0x7E00u;
   }
 #pragma unroll
   for (int k = 0; k < KD; ++k) even[k] |= odd[k] << 4;
@@ -283,8 +309,10 @@ struct ReadArgs {
   RowSplit split;
 };
 
-// VEC: rows of the outputs in aligned fours.
-template <int D, int BITS, int NG, bool VEC, typename T>
+// WIDE: rows of the outputs are aligned to 16 bytes.  Then fp16 goes out by eights, so that
+// the four lanes write 64 bytes in a row: two neighbours exchange their units, and one takes
+// the codes of even i, the other those of odd i.
+template <int D, int BITS, int NG, bool WIDE, typename T>
 __global__ __launch_bounds__(kThreads) void qcache_read_kernel(const ReadArgs p) {
   constexpr int kI = D / 16, kUnitBytes = kI * BITS / 8, KD = kUnitBytes;
   const seedlm_qcache_read_args& a = p.a;
@@ -308,21 +336,48 @@ __global__ __launch_bounds__(kThreads) void qcache_read_kernel(const ReadArgs p)
     load_dwords(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
   }
   T* out = (is_v ? static_cast<T*>(a.v_out) + t * a.v_stride
-                 : static_cast<T*>(a.k_out) + t * a.k_stride) + (int64_t)h * D + 4 * u;
+                 : static_cast<T*>(a.k_out) + t * a.k_stride) + (int64_t)h * D;
+  float s[NG], o[NG];
 #pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    const uint32_t so = pair[i * NG / kI];
-    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)so);
-    const float o = (float)__builtin_bit_cast(_Float16, (uint16_t)(so >> 16));
-    float x[4];
+  for (int n = 0; n < NG; ++n) {
+    s[n] = (float)__builtin_bit_cast(_Float16, (uint16_t)pair[n]);
+    o[n] = (float)__builtin_bit_cast(_Float16, (uint16_t)(pair[n] >> 16));
+  }
+  if constexpr (WIDE && sizeof(T) == 2) {
+    const int odd = u & 1;
+    uint32_t eight[2][KD];  // units 8 (u / 2) .. + 7, shifted to the codes of i % 2 == odd
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int byte = j * kUnitBytes + i * BITS / 8;
-      uint32_t d = code[byte / 4];
-      if (BITS == 4) d = (i % 2 ? d >> 4 : d) & 0x0F0F0F0Fu;
-      x[j] = o + s * (float)(d >> (8 * (byte % 4)) & 0xFF);
+    for (int k = 0; k < KD; ++k) {
+      const uint32_t mine = code[k] >> (odd * BITS), other = in_row<kSwapOne>(code[k]) >> (odd * BITS);
+      eight[0][k] = odd ? other : mine;
+      eight[1][k] = odd ? mine : other;
+      if (BITS == 4) eight[0][k] &= 0x0F0F0F0Fu, eight[1][k] &= 0x0F0F0F0Fu;
     }
-    store4<VEC>(out + 16 * i, x);
+#pragma unroll
+    for (int i = 0; i < kI; i += 2) {
+      const int n = i * NG / kI;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int byte = j % 4 * kUnitBytes + i * BITS / 8;
+        x[j] = o[n] + s[n] * (float)(eight[j / 4][byte / 4] >> (8 * (byte % 4)) & 0xFF);
+      }
+      store<8>(out + 16 * (i + odd) + 8 * (u >> 1), x);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int n = i * NG / kI;
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int byte = j * kUnitBytes + i * BITS / 8;
+        uint32_t d = code[byte / 4];
+        if (BITS == 4) d = (i % 2 ? d >> 4 : d) & 0x0F0F0F0Fu;
+        x[j] = o[n] + s[n] * (float)(d >> (8 * (byte % 4)) & 0xFF);
+      }
+      store4<WIDE>(out + 16 * i + 4 * u, x);
+    }
   }
 }
 
@@ -386,16 +441,17 @@ int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
 
 int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s) {
   const ReadArgs p{a, RowSplit(a.cache.kv_heads)};
-  const bool vec = (!a.k_out || fours(a.k_out, a.k_stride, a.y_dtype)) &&
-                   (!a.v_out || fours(a.v_out, a.v_stride, a.y_dtype));
+  const int64_t per = a.y_dtype == SEEDLM_F16 ? 8 : 4;  // elements of 16 bytes
+  const bool wide = (!a.k_out || (a.k_stride % per == 0 && aligned16(a.k_out))) &&
+                    (!a.v_out || (a.v_stride % per == 0 && aligned16(a.v_out)));
   const dim3 grid((a.tokens + p.split.tokens - 1) / p.split.tokens, p.split.passes);
   return with_row(a.cache, [&](auto d, auto bits, auto groups) {
     constexpr int kD = decltype(d)::value, kBits = decltype(bits)::value, kG = decltype(groups)::value;
     const bool f16 = a.y_dtype == SEEDLM_F16;
-    const auto kernel = vec ? (f16 ? qcache_read_kernel<kD, kBits, kG, true, __half>
-                                   : qcache_read_kernel<kD, kBits, kG, true, float>)
-                            : (f16 ? qcache_read_kernel<kD, kBits, kG, false, __half>
-                                   : qcache_read_kernel<kD, kBits, kG, false, float>);
+    const auto kernel = wide ? (f16 ? qcache_read_kernel<kD, kBits, kG, true, __half>
+                                    : qcache_read_kernel<kD, kBits, kG, true, float>)
+                             : (f16 ? qcache_read_kernel<kD, kBits, kG, false, __half>
+                                    : qcache_read_kernel<kD, kBits, kG, false, float>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, p);
     return launched();
   });
