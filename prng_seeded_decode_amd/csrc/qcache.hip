@@ -60,50 +60,93 @@ __device__ void store4(T* p, const float (&v)[4]) {
   }
 }
 
-// Elements e .. e + 3 of the head at `x`, turned by a token's cosines and sines.  Each
-// operation is rounded: codes next to a border must not depend on how the compiler
-// joins them.  VEC: pairs and angles lie in aligned fours.
-template <bool VEC, typename T>
-__device__ void turned4(const T* x, int e, int rot, bool interleaved, const float* cos,
-                        const float* sin, float (&y)[4]) {
+// A lane's elements 16i + 4u .. 16i + 4u + 3 of its head's row, in y[i], turned by a
+// token's cosines and sines where they lie below rot.  Each operation is rounded: codes
+// next to a border must not depend on how the compiler joins them.  All loads of a step
+// are requested before the first is used.
+template <int kI, typename T>
+__device__ void turn_fours(const T* x, int u, int rot, bool interleaved, bool is_k, const float* cos,
+                           const float* sin, float (&y)[kI][4]) {
 #pragma clang fp contract(off)
-  const int half = rot / 2;
-  if constexpr (VEC) {
-    load4<true>(x + e, y);
-    if (e >= rot) return;
-    if (interleaved) {
-      const float2 c = *reinterpret_cast<const float2*>(cos + e / 2);
-      const float2 s = *reinterpret_cast<const float2*>(sin + e / 2);
-      const float a0 = y[0], b0 = y[1], a1 = y[2], b1 = y[3];
-      y[0] = a0 * c.x - b0 * s.x, y[1] = b0 * c.x + a0 * s.x;
-      y[2] = a1 * c.y - b1 * s.y, y[3] = b1 * c.y + a1 * s.y;
-    } else {
-      const bool second = e >= half;
-      float o[4], c[4], s[4];
-      load4<true>(x + (second ? e - half : e + half), o);
-      load4<true>(cos + (second ? e - half : e), c);
-      load4<true>(sin + (second ? e - half : e), s);
+  if (interleaved) {
+    float2 c[kI], s[kI];
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int e = min(16 * i + 4 * u, rot - 4);
+      c[i] = *reinterpret_cast<const float2*>(cos + e / 2);
+      s[i] = *reinterpret_cast<const float2*>(sin + e / 2);
+    }
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const bool on = is_k && 16 * i + 4 * u < rot;
+      const float a0 = y[i][0], b0 = y[i][1], a1 = y[i][2], b1 = y[i][3];
+      const float z[4] = {a0 * c[i].x - b0 * s[i].x, b0 * c[i].x + a0 * s[i].x,
+                          a1 * c[i].y - b1 * s[i].y, b1 * c[i].y + a1 * s[i].y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[i][j] = on ? z[j] : y[i][j];
+    }
+  } else if (rot == 16 * kI) {  // the whole head: both halves of a pair are the lane's
+    float c[kI / 2][4], s[kI / 2][4];
+#pragma unroll
+    for (int i = 0; i < kI / 2; ++i) {
+      load4<true>(cos + 16 * i + 4 * u, c[i]);
+      load4<true>(sin + 16 * i + 4 * u, s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kI / 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float u = y[j] * c[j], w = o[j] * (second ? s[j] : -s[j]);
-        y[j] = u + w;
+        const float a = y[i][j], b = y[i + kI / 2][j];
+        const float za = a * c[i][j] - b * s[i][j], zb = b * c[i][j] + a * s[i][j];
+        y[i][j] = is_k ? za : a;
+        y[i + kI / 2][j] = is_k ? zb : b;
+      }
+  } else {  // the other half of a pair is in the caches
+    const int half = rot / 2;
+    constexpr int kStep = 4;
+#pragma unroll
+    for (int i0 = 0; i0 < kI; i0 += kStep) {
+      float o[kStep][4], c[kStep][4], s[kStep][4];
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const int e = min(16 * (i0 + i) + 4 * u, rot - 4);
+        load4<true>(x + (e >= half ? e - half : e + half), o[i]);
+        load4<true>(cos + (e >= half ? e - half : e), c[i]);
+        load4<true>(sin + (e >= half ? e - half : e), s[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const int e = 16 * (i0 + i) + 4 * u;
+        const bool on = is_k && e < rot;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float v = y[i0 + i][j] * c[i][j], w = o[i][j] * (e >= half ? s[i][j] : -s[i][j]);
+          y[i0 + i][j] = on ? v + w : y[i0 + i][j];
+        }
       }
     }
-  } else {
+  }
+}
+
+// The same for rows and angles at any address, element by element.
+template <int kI, typename T>
+__device__ void turn_each(const T* x, int u, int rot, bool interleaved, const float* cos,
+                          const float* sin, float (&y)[kI][4]) {
+#pragma clang fp contract(off)
+  const int half = rot / 2;
 #pragma unroll
-    for (int j = 0; j < 4; ++j, ++e) {
-      if (e >= rot) {
-        y[j] = (float)x[e];
-        continue;
-      }
+  for (int i = 0; i < kI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = 16 * i + 4 * u + j;
+      if (e >= rot) continue;
       const int pair = interleaved ? e / 2 : e % half;
       const bool second = interleaved ? e % 2 : e >= half;
       const float a = (float)x[interleaved ? 2 * pair : pair];
       const float b = (float)x[interleaved ? 2 * pair + 1 : pair + half];
       const float c = cos[pair], s = sin[pair];
-      y[j] = second ? b * c + a * s : a * c - b * s;
+      y[i][j] = second ? b * c + a * s : a * c - b * s;
     }
-  }
 }
 
 // The value of another lane of the same four; CTRL: its place, two bits a lane.
@@ -153,8 +196,8 @@ __device__ void store_dwords(void* p, const uint32_t (&v)[N]) {
 // Where a slot's row of a head lies: byte of its codes, number of its first pair.
 struct RowAt {
   int64_t codes, pair;
-  __device__ RowAt(const seedlm_qcache_t& c, int slot, int head) {
-    const int page = slot / c.page_size, nth = slot - page * c.page_size;
+  __device__ RowAt(const seedlm_qcache_t& c, Divisor page_size, int slot, int head) {
+    const int page = (int)page_size.of(slot), nth = slot - page * c.page_size;
     codes = page * c.page_stride + nth * c.token_stride + head * c.head_stride;
     pair = page * c.scale_page_stride + nth * c.scale_token_stride + head * c.scale_head_stride;
   }
@@ -183,6 +226,7 @@ struct RowSplit {
 struct AppendArgs {
   seedlm_qcache_append_args a;
   RowSplit split;
+  Divisor page_size;
   int units;            // units of a head of q
   Divisor token_units;  // units of a token of q
 };
@@ -232,20 +276,26 @@ __global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArg
   const int64_t t = t0 + token;
   if (t >= a.tokens) return;
   const int pos = a.positions[t], slot = a.slots[t];
-  if (pos < 0 || pos >= a.table_len || slot < 0 || slot >= c.pages * c.page_size) return;
   const bool is_v = row >= c.kv_heads;
   const int h = is_v ? row - c.kv_heads : row;
   const T* src = (is_v ? static_cast<const T*>(a.v) + t * a.v_stride
                        : static_cast<const T*>(a.k) + t * a.k_stride) + (int64_t)h * D;
-  const int rot = is_v ? 0 : a.rot;
+  float y[kI][4];
+#pragma unroll
+  for (int i = 0; i < kI; ++i) load4<VEC>(src + 16 * i + 4 * u, y[i]);
+  if (pos < 0 || pos >= a.table_len || slot < 0 || slot >= c.pages * c.page_size) return;
   const int64_t angle = (int64_t)pos * (a.rot / 2);
+  if constexpr (VEC) {
+    if (a.rot > 0 && __any(!is_v))
+      turn_fours<kI>(src, u, a.rot, a.interleaved, !is_v, a.cos + angle, a.sin + angle, y);
+  } else {
+    turn_each<kI>(src, u, is_v ? 0 : a.rot, a.interleaved, a.cos + angle, a.sin + angle, y);
+  }
   half2v x[kI][2];
 #pragma unroll
   for (int i = 0; i < kI; ++i) {
-    float y[4];
-    turned4<VEC>(src, 16 * i + 4 * u, rot, a.interleaved, a.cos + angle, a.sin + angle, y);
-    x[i][0] = half2v{(_Float16)y[0], (_Float16)y[1]};
-    x[i][1] = half2v{(_Float16)y[2], (_Float16)y[3]};
+    x[i][0] = half2v{(_Float16)y[i][0], (_Float16)y[i][1]};
+    x[i][1] = half2v{(_Float16)y[i][2], (_Float16)y[i][3]};
   }
 
   uint32_t even[KD], odd[KD], pair[NG];  // bytes of codes of even and of odd i
@@ -299,7 +349,7 @@ __global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArg
   }
 #pragma unroll
   for (int k = 0; k < KD; ++k) even[k] |= odd[k] << 4;
-  const RowAt at(c, slot, h);
+  const RowAt at(c, p.page_size, slot, h);
   store_dwords(static_cast<uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, even);
   if (u == 0) store_dwords(static_cast<uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
 }
@@ -307,6 +357,7 @@ __global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArg
 struct ReadArgs {
   seedlm_qcache_read_args a;
   RowSplit split;
+  Divisor page_size;
 };
 
 // WIDE: rows of the outputs are aligned to 16 bytes.  Then fp16 goes out by eights, so that
@@ -331,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void qcache_read_kernel(const ReadArgs p)
 #pragma unroll
   for (int n = 0; n < NG; ++n) pair[n] = 0;
   if (slot >= 0 && slot < c.pages * c.page_size) {
-    const RowAt at(c, slot, h);
+    const RowAt at(c, p.page_size, slot, h);
     load_dwords(static_cast<const uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, code);
     load_dwords(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
   }
@@ -420,7 +471,7 @@ int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
   const bool vec = fours(a.k, a.k_stride, a.x_dtype) && fours(a.v, a.v_stride, a.x_dtype) &&
                    a.rot % 8 == 0 && aligned16(a.cos) && aligned16(a.sin);
   const bool wide = vec && wide_units(a);
-  AppendArgs p{a, RowSplit(a.cache.kv_heads), wide ? D / 16 : D / 2, {}};
+  AppendArgs p{a, RowSplit(a.cache.kv_heads), divisor((uint32_t)a.cache.page_size), wide ? D / 16 : D / 2, {}};
   if (a.heads > 1024) p.split.tokens = 1;  // the grid's second dimension is short
   const int token_units = a.heads * p.units;
   p.token_units = divisor((uint32_t)token_units);
@@ -440,7 +491,7 @@ int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
 }
 
 int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s) {
-  const ReadArgs p{a, RowSplit(a.cache.kv_heads)};
+  const ReadArgs p{a, RowSplit(a.cache.kv_heads), divisor((uint32_t)a.cache.page_size)};
   const int64_t per = a.y_dtype == SEEDLM_F16 ? 8 : 4;  // elements of 16 bytes
   const bool wide = (!a.k_out || (a.k_stride % per == 0 && aligned16(a.k_out))) &&
                     (!a.v_out || (a.v_stride % per == 0 && aligned16(a.v_out)));
