@@ -46,6 +46,7 @@ namespace qattend {
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half4v __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
@@ -66,7 +67,8 @@ struct Args {
   uint32_t page_unit, token_unit;  // strides of codes in units of 16 bytes
   uint32_t page_pair, token_pair;  // strides of pairs in rows of pairs
   Divisor page_size;
-  int32_t* ends;  // [queries] inclusive sums of units, for the join
+  int32_t* ends;    // [queries] inclusive sums of units, for the join
+  int32_t* firsts;  // [queries] the first query of each one's item, for the join
   float2* ml;     // [2 * slots][kv_heads * qtiles][16] maximum (log2) and sum
   float* acc;     // [2 * slots][kv_heads * qtiles][16][D]
 };
@@ -77,16 +79,20 @@ __device__ inline int length_of(const Args& p, int b) {
   return !p.a.rows || (uint32_t)p.a.rows[b] < (uint32_t)p.a.table_rows ? len : 0;
 }
 
-// Whether query b is the first of its item.
-__device__ inline bool starts_item(const Args& p, int b) {
-  return p.shared == 1 || b % p.shared == 0 || p.a.rows[b] != p.a.rows[b - 1];
+// What is kept of query b in LDS: its tokens, negative (-1 - tokens) where it goes on with
+// the item of the query before.
+__device__ inline int item_entry(const Args& p, int b) {
+  const int len = length_of(p, b);
+  const bool goes_on = p.shared > 1 && b % p.shared != 0 && p.a.rows[b] == p.a.rows[b - 1];
+  return goes_on ? -1 - len : len;
 }
 
-// The queries of the item that starts with b, and the longest of their lengths.
-__device__ inline int2 item_of(const Args& p, int b) {
-  int n = 1, len = length_of(p, b);
-  while (b + n < p.a.queries && !starts_item(p, b + n)) len = max(len, length_of(p, b + n)), ++n;
-  return make_int2(n, len);
+// The queries of the item whose first entry is e[0], of n entries, and the longest of
+// their lengths.
+__device__ inline int2 item_of(const int32_t* e, int n) {
+  int k = 1, len = e[0];
+  while (k < n && e[k] < 0) len = max(len, -1 - e[k]), ++k;
+  return make_int2(k, len);
 }
 
 __device__ inline half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
@@ -196,10 +202,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
   constexpr int kSteps = R::kSteps, kAccs = R::kAccs, KD = R::KD, VD = R::VD;
   constexpr int kStride = D + 4;  // LDS row stride (floats)
   __shared__ __align__(16) uint32_t s_off[kWaves][kTile];
-  __shared__ __align__(16) uint32_t s_pair[kWaves][2 * kTile * NG];
+  __shared__ __align__(16) uint32_t s_pair[kWaves][NG][2 * kTile];
   __shared__ float2 s_ml[kWaves][16];
   __shared__ __align__(16) float s_acc[kWaves][16][kStride];
-  extern __shared__ int32_t s_ends[];  // of the items' units
+  extern __shared__ int32_t s_ends[];  // inclusive sums of the items' units, then the entries
   const seedlm_qcache_attend_args& a = p.a;
   const seedlm_qcache_t& c = a.cache;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -209,28 +215,41 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
   const int head0 = hk * p.group + qt * 16;
 
   int unit = 0, unit_end = 1, run_begin = 0;
+  int32_t* s_entry = s_ends;
   if (p.slots > 0) {
+    s_entry = s_ends + a.queries;
+    for (int b = threadIdx.x; b < a.queries; b += kThreads) s_entry[b] = item_entry(p, b);
+    __syncthreads();
     sum_units<kThreads>(a.queries, s_ends, [&](int b) {
-      return starts_item(p, b) ? (item_of(p, b).y + kUnit - 1) / kUnit : 0;
+      return s_entry[b] < 0 ? 0 : (item_of(s_entry + b, a.queries - b).y + kUnit - 1) / kUnit;
     });
     const int units = s_ends[a.queries - 1];
     if (blockIdx.x == 0 && blockIdx.y == 0)
-      for (int b = threadIdx.x; b < a.queries; b += kThreads) p.ends[b] = s_ends[b];
+      for (int b = threadIdx.x; b < a.queries; b += kThreads) {
+        int first = b;
+        while (s_entry[first] < 0) --first;
+        p.ends[b] = s_ends[b];
+        p.firsts[b] = first;
+      }
     const int slots = min(p.slots, units);  // none is empty
     if ((int)blockIdx.y >= slots) return;
     run_begin = unit = slot_begin(blockIdx.y, units, slots);
     unit_end = slot_begin(blockIdx.y + 1, units, slots);
-  } else if (!starts_item(p, blockIdx.y)) {
-    return;
+  } else {
+    const int n = min(p.shared, a.queries - (int)blockIdx.y);
+    if ((int)threadIdx.x < n) s_entry[threadIdx.x] = item_entry(p, blockIdx.y + threadIdx.x);
+    __syncthreads();
+    if (s_entry[0] < 0) return;
   }
   while (unit < unit_end) {
     // The next item of the run and the tokens of it that lie in the run.
     int first_query = blockIdx.y, begin = 0, end;
     bool whole = true;
     const bool starts_run = unit == run_begin;
-    if (p.slots > 0) first_query = request_of(s_ends, a.queries, unit);
-    const int2 item = item_of(p, first_query);
+    int2 item;
     if (p.slots > 0) {
+      first_query = request_of(s_ends, a.queries, unit);
+      item = item_of(s_entry + first_query, a.queries - first_query);
       const int u0 = first_query > 0 ? s_ends[first_query - 1] : 0, u1 = s_ends[first_query];
       const int upto = min(u1, unit_end);
       begin = (unit - u0) * kUnit;
@@ -238,6 +257,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       whole = unit == u0 && upto == u1;
       unit = upto;
     } else {
+      item = item_of(s_entry, min(p.shared, a.queries - (int)blockIdx.y));
       end = item.y;
       unit = unit_end;
     }
@@ -246,50 +266,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
     const int columns = item.x * heads;
     const int column = min(m, columns - 1);
     const int query = first_query + column / heads, head = head0 + column % heads;
-    const int length = m < columns ? length_of(p, query) : item.y;
-
-    // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
-    // (0..3), in the order of Row::keys.  The row's largest element goes into [2^9, 2^10),
-    // so that low parts and sixteenths have all their bits.
-    half8 qh[kSteps], ql[WIDE ? kSteps : 1];
-    float sc = a.scale * kLog2e;
-    float qsum[NG];  // of a group's elements, in the units of its products with codes
-    {
-      const T* q = static_cast<const T*>(a.q) + (int64_t)query * a.q_stride + (int64_t)head * D + g * 4;
-      float f[kSteps][8], top = 0.f;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[s][(j / 2) * 4 + h * 2 + j % 2] = (float)q[16 * (2 * s + h) + j];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[s][j]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      int e = 10;
-      if (top > 0.f && top < INFINITY) (void)frexpf(top, &e);
-      const int up = 10 - e;
-      sc = ldexpf(sc, 24 - up);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = m < columns ? ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up) : 0.f;
-          qh[s][j] = (_Float16)x;
-          if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
-        }
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        floatx4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = j * kSteps / NG; i < (j + 1) * kSteps / NG; ++i) {
-          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), qh[i], s, 0, 0, 0);
-          if constexpr (WIDE) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), ql[i], s, 0, 0, 0);
-        }
-        qsum[j] = s[0];
-      }
+    int length = item.y;
+    if (m < columns) {
+      length = s_entry[p.slots > 0 ? query : query - first_query];
+      length = length < 0 ? -1 - length : length;
     }
 
     const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
@@ -355,6 +335,59 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       for (int j = 0; j < 8; ++j) load_codes<R::kUnitBytes>(vbase + (uint64_t)voff[j] * 16, t.v[j]);
     };
 
+    Tile even, odd;
+    if (tiles > 0) {
+      look_up(0);
+      request(even, 1);
+    }
+
+    // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
+    // (0..3), in the order of Row::keys.  The row's largest element goes into [2^9, 2^10),
+    // so that low parts and sixteenths have all their bits.
+    half8 qh[kSteps], ql[WIDE ? kSteps : 1];
+    float sc = a.scale * kLog2e;
+    float qsum[NG];  // of a group's elements, in the units of its products with codes
+    {
+      const T* q = static_cast<const T*>(a.q) + (int64_t)query * a.q_stride + (int64_t)head * D + g * 4;
+      float f[kSteps][8], most = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          using Four = std::conditional_t<WIDE, floatx4, half4v>;
+          const Four v = *reinterpret_cast<const Four*>(q + 16 * (2 * s + h));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[s][(j / 2) * 4 + h * 2 + j % 2] = (float)v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(f[s][j]));
+      }
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = fmaxf(most, __shfl_xor(most, 32));
+      int e = 10;
+      if (most > 0.f && most < INFINITY) (void)frexpf(most, &e);
+      const int up = 10 - e;
+      sc = ldexpf(sc, 24 - up);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = m < columns ? ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up) : 0.f;
+          qh[s][j] = (_Float16)x;
+          if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
+        }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = j * kSteps / NG; i < (j + 1) * kSteps / NG; ++i) {
+          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), qh[i], s, 0, 0, 0);
+          if constexpr (WIDE) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), ql[i], s, 0, 0, 0);
+        }
+        qsum[j] = s[0];
+      }
+    }
+
     float top = -INFINITY, base = -INFINITY;  // running maximum (log2), and with E added
     float sum = 0.f, osum[NG];  // this lane's share of the weights, and of them times offsets
     floatx4 acc[kAccs];
@@ -366,69 +399,62 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
     for (int i = 0; i < kAccs; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 
     auto compute = [&](const Tile& t, int i) {
-      floatx4 s[NG][2];
-#pragma unroll
-      for (int j = 0; j < NG; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[j][h] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = j * kSteps / NG; k < (j + 1) * kSteps / NG; ++k) {
-            const half8 x = R::keys(t.k[h], k);
-            s[j][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, qh[k], s[j][h], 0, 0, 0);
-            if constexpr (WIDE)
-              s[j][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, ql[k], s[j][h], 0, 0, 0);
-          }
-        }
       // Pairs: none of a token that does not exist, NaN for what is not finite.
       uint32_t e = 0;
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        uint32_t x = t.ok ? t.pair[j] : 0;
-        const uint32_t es = x & 0x7C00u, eo = x & 0x7C000000u;
-        if (es == 0x7C00u || eo == 0x7C000000u) x = 0x7E007E00u;
+      for (int n = 0; n < NG; ++n) {
+        uint32_t so = t.ok ? t.pair[n] : 0;
+        const uint32_t es = so & 0x7C00u, eo = so & 0x7C000000u;
+        if (es == 0x7C00u || eo == 0x7C000000u) so = 0x7E007E00u;
         else e = max(e, es);
-        s_pair[wave][lane * NG + j] = x;
+        s_pair[wave][n][lane] = so;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      auto read_pairs = [&](int at, uint32_t (&out)[8][NG]) {
+      // The pairs of group n of this lane's 8 tokens, of the keys (at 0) or the values (32).
+      auto read_pairs = [&](int n, int at, uint32_t (&out)[8]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          const v4u v = *reinterpret_cast<const v4u*>(&s_pair[wave][n][at + 16 * h + 4 * g]);
 #pragma unroll
-          for (int j = 0; j < NG; ++j) {
-            const v4u v = *reinterpret_cast<const v4u*>(&s_pair[wave][(at + 16 * h + 4 * g) * NG + 4 * j]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) out[4 * h + (4 * j + x) / NG][(4 * j + x) % NG] = v[x];
-          }
+          for (int j = 0; j < 4; ++j) out[4 * h + j] = v[j];
+        }
       };
-      uint32_t kp[8][NG], vp[8][NG];
-      read_pairs(0, kp);
-      read_pairs(kTile, vp);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
 
       float x[8], most = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float y = 0.f;
+      for (int n = 0; n < NG; ++n) {
+        uint32_t kp[8];
+        read_pairs(n, 0, kp);
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const half2v so = as_half2(kp[j][n]);
-          y += (float)so[1] * qsum[n];
-          y += (float)so[0] * s[n][j >> 2][j & 3];
+        for (int h = 0; h < 2; ++h) {
+          floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = n * kSteps / NG; k < (n + 1) * kSteps / NG; ++k) {
+            const half8 codes = R::keys(t.k[h], k);
+            s = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, qh[k], s, 0, 0, 0);
+            if constexpr (WIDE) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes, ql[k], s, 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const half2v so = as_half2(kp[4 * h + j]);
+            float& y = x[4 * h + j];
+            y = n == 0 ? (float)so[1] * qsum[n] : y + (float)so[1] * qsum[n];
+            y += (float)so[0] * s[j];
+          }
         }
-        x[j] = y * sc;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= sc;
       const int tile_first = first + i * kUnit;
-      if (!t.whole || __any(tile_first + kTile > length)) {
+      const bool masked = !t.whole || __any(tile_first + kTile > length);
+      uint32_t on = t.live;
+      if (masked) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int tok = tile_first + (j >> 2) * 16 + 4 * g + (j & 3);
-          const bool on = ((t.live >> j) & 1) && tok < length;
-          x[j] = on ? x[j] : -INFINITY;
-#pragma unroll
-          for (int n = 0; n < NG; ++n) vp[j][n] = on ? vp[j][n] : 0;
+          on &= ~((uint32_t)(tok >= length) << j);
+          x[j] = (on >> j) & 1 ? x[j] : -INFINITY;
         }
       }
 #pragma unroll
@@ -461,10 +487,16 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       for (int j = 0; j < 8; ++j) sum += x[j];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
+        uint32_t vp[8];
+        read_pairs(n, kTile, vp);
+        if (masked) {  // NaN of a token that this column does not attend to
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vp[j] = (on >> j) & 1 ? vp[j] : 0;
+        }
         v4u ph, pl;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const half2v a0 = as_half2(vp[2 * w][n]), a1 = as_half2(vp[2 * w + 1][n]);
+          const half2v a0 = as_half2(vp[2 * w]), a1 = as_half2(vp[2 * w + 1]);
           osum[n] += x[2 * w] * (float)a0[1];
           osum[n] += x[2 * w + 1] * (float)a1[1];
           const float w0 = x[2 * w] * (float)a0[0], w1 = x[2 * w + 1] * (float)a1[0];
@@ -479,13 +511,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
           acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(pl), acc[k], 0, 0, 0);
         }
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     };
 
-    Tile even, odd;
-    if (tiles > 0) {
-      look_up(0);
-      request(even, 1);
-    }
     for (int i = 0; i < tiles; i += 2) {
       if (i + 1 < tiles) request(odd, i + 2);
       compute(even, i);
@@ -549,8 +578,7 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
   __shared__ __align__(16) floatx4 s_part[kGroups][kLanes];
   const seedlm_qcache_attend_args& a = p.a;
   const int query = blockIdx.y, head = blockIdx.x;
-  int b = query;  // the item's first query
-  while (!starts_item(p, b)) --b;
+  const int b = p.firsts[query];  // the item's first query
   const int units = p.ends[a.queries - 1], slots = min(p.slots, units);
   const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
   // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
@@ -603,7 +631,7 @@ int run_groups(const Args& p, hipStream_t s) {
   const bool split = p.slots > 0;
   hipLaunchKernelGGL((qcache_attend_kernel<D, BITS, NG, WIDE>),
                      dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries), dim3(kThreads),
-                     split ? a.queries * sizeof(int32_t) : 0, s, p);
+                     (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
   if (split)
     hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE>), dim3(a.heads, a.queries),
                        dim3(kThreads), 0, s, p);

@@ -42,7 +42,7 @@ Scratch scratch_of(const seedlm_qcache_attend_args& a) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Scratch r;
   r.ends = 0;
-  r.ml = up((size_t)a.queries * sizeof(int32_t));
+  r.ml = up((size_t)2 * a.queries * sizeof(int32_t));
   r.acc = r.ml + up(n * sizeof(float2));
   r.bytes = n == 0 ? 0 : r.acc + n * a.cache.head_dim * sizeof(float);
   return r;
@@ -71,6 +71,7 @@ int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipS
   char* base = static_cast<char*>(scratch);
   if (base) {
     p.ends = reinterpret_cast<int32_t*>(base + r.ends);
+    p.firsts = p.ends + a.queries;
     p.ml = reinterpret_cast<float2*>(base + r.ml);
     p.acc = reinterpret_cast<float*>(base + r.acc);
   }
