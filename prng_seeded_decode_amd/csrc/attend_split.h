@@ -9,11 +9,16 @@ namespace seedlm {
 
 // The first unit of a slot among `units`, and the slot of a unit: the largest i
 // with i * units / slots <= u, that is i * units < (u + 1) * slots.
+// (A 64-bit division takes half a microsecond, so it is left to the largest numbers.)
 __device__ inline int slot_begin(int slot, int units, int slots) {
-  return (int)((int64_t)slot * units / slots);
+  const uint64_t x = (uint64_t)slot * (uint32_t)units;
+  if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)slots);
+  return (int)(x / (uint32_t)slots);
 }
 __device__ inline int slot_of(int u, int units, int slots) {
-  return (int)((((int64_t)u + 1) * slots - 1) / units);
+  const uint64_t x = ((uint64_t)u + 1) * (uint32_t)slots - 1;
+  if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)units);
+  return (int)(x / (uint32_t)units);
 }
 
 // Inclusive sums of units_of(0), ..., units_of(n - 1) into ends[0..n), by all

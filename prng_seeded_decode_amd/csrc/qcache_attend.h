@@ -102,6 +102,21 @@ __device__ inline uint32_t pack_rtz(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
 
+// The largest x of lanes l, l ^ 16, l ^ 32 and l ^ 48.
+__device__ inline float max_of_column(float x) {
+  auto largest = [](auto swapped) {
+    const uint32_t a = swapped[0], b = swapped[1];
+    return fmaxf(__uint_as_float(a), __uint_as_float(b));
+  };
+  uint32_t u = __float_as_uint(x);
+  u = __float_as_uint(largest(__builtin_amdgcn_permlane16_swap(u, u, false, false)));
+  return largest(__builtin_amdgcn_permlane32_swap(u, u, false, false));
+}
+
+// Keeps what a rare branch does in the branch: the compiler would rather do it always
+// and select.
+__device__ inline void rare() { asm volatile(""); }
+
 template <typename T>
 __device__ void store4(T* p, floatx4 v) {
   if constexpr (sizeof(T) == 4) {
@@ -190,12 +205,13 @@ __device__ void load_codes(const uint8_t* p, uint32_t (&out)[N]) {
 
 // Waves of the kernel per SIMD, and so workgroups per compute unit: what the registers
 // of each form allow.
-__host__ __device__ constexpr int waves_per_simd(int D, int bits, bool wide) {
-  return D == 256 ? (bits == 8 ? 1 : 2) : (D == 128 && (bits == 8 || wide) ? 2 : 3);
+__host__ __device__ constexpr int waves_per_simd(int D, int bits, int groups, bool wide) {
+  if (D == 256) return bits == 8 || wide || groups > 1 ? 1 : 2;
+  return D == 128 && (bits == 8 || wide || groups > 1) ? 2 : 3;
 }
 
 template <int D, int BITS, int NG, bool WIDE>
-__global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcache_attend_kernel(
+__global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void qcache_attend_kernel(
     const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
   using R = Row<D, BITS>;
@@ -262,15 +278,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       unit = unit_end;
     }
 
-    // This lane's column: a query and a head.
+    // This lane's column: a query and a head; columns past the last repeat it.
     const int columns = item.x * heads;
     const int column = min(m, columns - 1);
     const int query = first_query + column / heads, head = head0 + column % heads;
-    int length = item.y;
-    if (m < columns) {
-      length = s_entry[p.slots > 0 ? query : query - first_query];
-      length = length < 0 ? -1 - length : length;
-    }
+    int length = s_entry[p.slots > 0 ? query : query - first_query];
+    length = length < 0 ? -1 - length : length;
 
     const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
     const uint8_t* vbase = static_cast<const uint8_t*>(c.v) + hk * c.head_stride + m * R::kUnitBytes;
@@ -304,7 +317,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       const uint32_t off = (uint32_t)page * p.page_unit + (uint32_t)nth * p.token_unit;
       const uint32_t row = ok ? (uint32_t)page * p.page_pair + (uint32_t)nth * p.token_pair : 0;
       if (lane < kTile) s_off[wave][lane] = ok ? off : kNoToken;
-      if (next < tiles) look_up(next);
+      look_up(next);
       t.ok = ok;
       t.whole = !__any(!ok);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -319,6 +332,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       __builtin_amdgcn_wave_barrier();
       t.live = 0xFF;
       if (!t.whole) {  // tokens that do not exist read token 0 of page 0 and are masked
+        rare();
         t.live = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -342,40 +356,88 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
     }
 
     // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
-    // (0..3), in the order of Row::keys.  The row's largest element goes into [2^9, 2^10),
-    // so that low parts and sixteenths have all their bits.
+    // (0..3), in the order of Row::keys.
     half8 qh[kSteps], ql[WIDE ? kSteps : 1];
-    float sc = a.scale * kLog2e;
+    float sc = a.scale * kLog2e * 0x1p24f;  // of products, to scores in powers of 2
     float qsum[NG];  // of a group's elements, in the units of its products with codes
     {
+      using Four = std::conditional_t<WIDE, floatx4, v2u>;
       const T* q = static_cast<const T*>(a.q) + (int64_t)query * a.q_stride + (int64_t)head * D + g * 4;
-      float f[kSteps][8], most = 0.f;
+      Four raw[2 * kSteps];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int s = 0; s < 2 * kSteps; ++s) raw[s] = *reinterpret_cast<const Four*>(q + 16 * s);
+      // fp16 goes in as it is and divided by 16 where that keeps all bits that count: where
+      // the row's largest element is at least 2, so that what falls below fp16's normal
+      // numbers is rounded to 2^-22 of that.  Other rows, and fp32 ones, are multiplied by a power
+      // of two that puts their largest element into [2^9, 2^10).
+      bool as_is = false;
+      if constexpr (!WIDE) {
+        half2v most = {0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          using Four = std::conditional_t<WIDE, floatx4, half4v>;
-          const Four v = *reinterpret_cast<const Four*>(q + 16 * (2 * s + h));
+        for (int s = 0; s < 2 * kSteps; ++s)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[s][(j / 2) * 4 + h * 2 + j % 2] = (float)v[j];
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = raw[s][j];
+            most = __builtin_elementwise_max(most, as_half2(w & 0x7FFF7FFFu));
+          }
+        const float top = max_of_column(fmaxf((float)most[0], (float)most[1]));
+        as_is = BITS == 8 || !__any(!(top >= 2.f));
+        const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t odd[2] = {raw[2 * s + 1][0], raw[2 * s + 1][1]};
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (BITS == 4) odd[j] = __builtin_bit_cast(uint32_t, as_half2(odd[j]) * sixteenth);
+          qh[s] = as_half8(v4u{raw[2 * s][0], odd[0], raw[2 * s][1], odd[1]});
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(f[s][j]));
       }
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
-      int e = 10;
-      if (most > 0.f && most < INFINITY) (void)frexpf(most, &e);
-      const int up = 10 - e;
-      sc = ldexpf(sc, 24 - up);
+      if (!as_is) {
+        rare();
+        float f[kSteps][8], most = 0.f;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
+        for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = m < columns ? ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up) : 0.f;
-          qh[s][j] = (_Float16)x;
-          if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float x;
+              if constexpr (WIDE) {
+                x = raw[2 * s + h][j];
+              } else {
+                const uint32_t w = raw[2 * s + h][j / 2];
+                x = (float)as_half2(w)[j % 2];
+              }
+              f[s][(j / 2) * 4 + h * 2 + j % 2] = x;
+              most = fmaxf(most, fabsf(x));
+            }
         }
+        most = max_of_column(most);
+        int e = 10;
+        if (most > 0.f && most < INFINITY) (void)frexpf(most, &e);
+        const int up = 10 - e;
+        sc = ldexpf(a.scale * kLog2e, 24 - up);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up);
+            qh[s][j] = (_Float16)x;
+            if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
+          }
+      }
+      // Scores times sc have to grow with the products: a negative scale turns the query, and
+      // one of 0 leaves nothing of it.
+      if (!(sc > 0.f)) {
+        rare();
+        const _Float16 sign = sc < 0.f ? -1.f : 0.f;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          qh[s] *= sign;
+          if constexpr (WIDE) ql[s] *= sign;
+        }
+        sc = sc < 0.f ? -sc : 1.f;
+      }
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         floatx4 s = {0.f, 0.f, 0.f, 0.f};
@@ -444,12 +506,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
           }
         }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= sc;
       const int tile_first = first + i * kUnit;
       const bool masked = !t.whole || __any(tile_first + kTile > length);
       uint32_t on = t.live;
       if (masked) {
+        rare();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int tok = tile_first + (j >> 2) * 16 + 4 * g + (j & 3);
@@ -459,10 +520,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
+      most = max_of_column(most) * sc;
       const bool grows = __any(lane >= kTile && e > largest);
       if (grows) {
+        rare();
         if (lane < kTile) e = 0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) e = max(e, (uint32_t)__shfl_xor((int)e, d));
@@ -470,6 +531,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
         E = (float)(int)(largest >> 10) - 14.f;
       }
       if (grows || __any(most > top)) {
+        rare();
         top = fmaxf(top, most);
         const float up = top + E;
         const float shrink = up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up);
@@ -482,7 +544,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       }
       const float ref = base == -INFINITY ? 0.f : base - 15.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j] - ref);
+      for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], sc, -ref));
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += x[j];
 #pragma unroll
@@ -490,6 +552,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
         uint32_t vp[8];
         read_pairs(n, kTile, vp);
         if (masked) {  // NaN of a token that this column does not attend to
+          rare();
 #pragma unroll
           for (int j = 0; j < 8; ++j) vp[j] = (on >> j) & 1 ? vp[j] : 0;
         }
@@ -515,13 +578,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, WIDE)) void qcach
       __builtin_amdgcn_wave_barrier();
     };
 
-    for (int i = 0; i < tiles; i += 2) {
-      if (i + 1 < tiles) request(odd, i + 2);
+    // (A request past the last tile reads the masked token of page 0; without it the paths
+    // through the loop would have to wait for one another's loads.)
+    for (int i = 0; i < tiles; ++i) {
+      request(odd, i + 2);
       compute(even, i);
-      if (i + 1 < tiles) {
-        if (i + 2 < tiles) request(even, i + 3);
-        compute(odd, i + 1);
-      }
+      if (++i >= tiles) break;
+      request(even, i + 2);
+      compute(odd, i);
     }
 
     // Join the four waves.

@@ -27,7 +27,8 @@ bool unsplit(const seedlm_qcache_attend_args& a) {
 int slots_of(const seedlm_qcache_attend_args& a) {
   if (unsplit(a)) return 0;
   const int held = device_cu_count() *
-                   waves_per_simd(a.cache.head_dim, a.cache.bits, a.x_dtype == SEEDLM_F32);
+                   waves_per_simd(a.cache.head_dim, a.cache.bits, a.cache.head_dim / a.cache.group,
+                                  a.x_dtype == SEEDLM_F32);
   const int across = a.cache.kv_heads * qtiles_of(a);
   return (held + across - 1) / across;
 }
