@@ -54,6 +54,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;              // tokens of a wave's step
 constexpr int kUnit = kWaves * kTile;  // tokens of a workgroup's step
+constexpr int kItemUnits = 4;          // what starting an item counts for in the split
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -94,6 +95,9 @@ __device__ inline int2 item_of(const int32_t* e, int n) {
   while (k < n && e[k] < 0) len = max(len, -1 - e[k]), ++k;
   return make_int2(k, len);
 }
+
+// Units of an item in the split.
+__device__ inline int units_of(int len) { return len > 0 ? kItemUnits + (len + kUnit - 1) / kUnit : 0; }
 
 __device__ inline half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
 __device__ inline half2v as_half2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
@@ -183,20 +187,26 @@ struct Row {
   }
 };
 
-// Bytes [at, at + 4 N) as N dwords, or 2 bytes as one.
-template <int BYTES, int N>
+template <bool STREAM, typename T>
+__device__ T load(const uint8_t* p) {
+  const T* q = reinterpret_cast<const T*>(p);
+  return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
+
+// BYTES bytes at p as N dwords (2 bytes as one); STREAM: past the caches.
+template <int BYTES, bool STREAM, int N>
 __device__ void load_codes(const uint8_t* p, uint32_t (&out)[N]) {
   if constexpr (BYTES == 2) {
-    out[0] = *reinterpret_cast<const uint16_t*>(p);
+    out[0] = load<STREAM, uint16_t>(p);
   } else if constexpr (BYTES == 4) {
-    out[0] = *reinterpret_cast<const uint32_t*>(p);
+    out[0] = load<STREAM, uint32_t>(p);
   } else if constexpr (BYTES == 8) {
-    const v2u v = *reinterpret_cast<const v2u*>(p);
+    const v2u v = load<STREAM, v2u>(p);
     out[0] = v[0], out[1] = v[1];
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      const v4u v = reinterpret_cast<const v4u*>(p)[i];
+      const v4u v = load<STREAM, v4u>(p + 16 * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) out[4 * i + j] = v[j];
     }
@@ -210,7 +220,8 @@ __host__ __device__ constexpr int waves_per_simd(int D, int bits, int groups, bo
   return D == 128 && (bits == 8 || wide || groups > 1) ? 2 : 3;
 }
 
-template <int D, int BITS, int NG, bool WIDE>
+// WIDE: fp32 q and out, else fp16.  STREAM: codes pass the caches.
+template <int D, int BITS, int NG, bool WIDE, bool STREAM>
 __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void qcache_attend_kernel(
     const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
@@ -237,7 +248,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     for (int b = threadIdx.x; b < a.queries; b += kThreads) s_entry[b] = item_entry(p, b);
     __syncthreads();
     sum_units<kThreads>(a.queries, s_ends, [&](int b) {
-      return s_entry[b] < 0 ? 0 : (item_of(s_entry + b, a.queries - b).y + kUnit - 1) / kUnit;
+      return s_entry[b] < 0 ? 0 : units_of(item_of(s_entry + b, a.queries - b).y);
     });
     const int units = s_ends[a.queries - 1];
     if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -268,10 +279,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       item = item_of(s_entry + first_query, a.queries - first_query);
       const int u0 = first_query > 0 ? s_ends[first_query - 1] : 0, u1 = s_ends[first_query];
       const int upto = min(u1, unit_end);
-      begin = (unit - u0) * kUnit;
-      end = min(item.y, (upto - u0) * kUnit);
-      whole = unit == u0 && upto == u1;
+      // of the item's units those that stand for its start hold no tokens
+      begin = max(unit - u0 - kItemUnits, 0) * kUnit;
+      end = min(item.y, (upto - u0 - kItemUnits) * kUnit);
+      whole = begin == 0 && upto == u1;
       unit = upto;
+      if (begin >= end) continue;  // the run ends before the item's tokens do begin
     } else {
       item = item_of(s_entry, min(p.shared, a.queries - (int)blockIdx.y));
       end = item.y;
@@ -343,10 +356,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         for (int h = 0; h < 2; ++h) koff[h] = koff[h] != kNoToken ? koff[h] : 0;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_codes<R::kBytes / 4>(kbase + (uint64_t)koff[h] * 16, t.k[h]);
-      load_codes<4 * NG>(reinterpret_cast<const uint8_t*>(pairs + (uint64_t)row * NG), t.pair);
+      for (int h = 0; h < 2; ++h) load_codes<R::kBytes / 4, STREAM>(kbase + (uint64_t)koff[h] * 16, t.k[h]);
+      load_codes<4 * NG, false>(reinterpret_cast<const uint8_t*>(pairs + (uint64_t)row * NG), t.pair);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) load_codes<R::kUnitBytes>(vbase + (uint64_t)voff[j] * 16, t.v[j]);
+      for (int j = 0; j < 8; ++j) load_codes<R::kUnitBytes, STREAM>(vbase + (uint64_t)voff[j] * 16, t.v[j]);
     };
 
     Tile even, odd;
@@ -633,29 +646,31 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 }
 
 // Joins the pieces of one query and head, and writes zeros for queries without any.
-// Every wave forms the maximum and the sum itself; groups of D/4 lanes take the pieces
-// in turn.
-template <int D, bool WIDE>
+// THREADS threads take a head, of 4 in a workgroup or alone; every wave forms the maximum
+// and the sum itself, and groups of D/4 lanes take the pieces in turn.
+template <int D, bool WIDE, int THREADS>
 __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
-  constexpr int kLanes = D / 4, kGroups = kThreads / kLanes;
-  __shared__ __align__(16) floatx4 s_part[kGroups][kLanes];
+  constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kHeads = kThreads / THREADS;
+  __shared__ __align__(16) floatx4 s_part[kHeads][kGroups][kLanes];
   const seedlm_qcache_attend_args& a = p.a;
-  const int query = blockIdx.y, head = blockIdx.x;
+  const int thread = threadIdx.x % THREADS, nth = threadIdx.x / THREADS;
+  const int query = blockIdx.y, head = blockIdx.x * kHeads + nth;
+  if (head >= a.heads) return;
   const int b = p.firsts[query];  // the item's first query
   const int units = p.ends[a.queries - 1], slots = min(p.slots, units);
   const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
   // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
-  // but the first they start the slot's run.
+  // but the first, whose run may have begun before the item, they start the slot's run.
   int first_slot = 0, pieces = 0, skip = 0;
   if (u1 > u0) {
-    first_slot = slot_of(u0, units, slots);
+    first_slot = slot_of(u0 + kItemUnits, units, slots);
     pieces = slot_of(u1 - 1, units, slots) - first_slot + 1;
-    skip = slot_begin(first_slot, units, slots) != u0;
+    skip = slot_begin(first_slot, units, slots) < u0;
   }
   if (pieces == 1) return;
   T* out = static_cast<T*>(a.out) + (int64_t)query * a.out_stride + (int64_t)head * D;
-  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int lane = thread % kLanes, group = thread / kLanes;
   const int in_group = head % p.group, heads = min(16, p.group - in_group / 16 * 16);
   const int block = head / p.group * p.qtiles + in_group / 16;
   const int column = (query - b) * heads + in_group % 16;
@@ -681,23 +696,43 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
     const float f = __builtin_amdgcn_exp2f(p.ml[i].x - ref);
     o += f * *reinterpret_cast<const floatx4*>(p.acc + i * D + lane * 4);
   }
-  s_part[group][lane] = o;
-  __syncthreads();
+  s_part[nth][group][lane] = o;
+  if constexpr (THREADS == kThreads) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
   if (group != 0) return;
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) o += s_part[k][lane];
+  for (int k = 1; k < kGroups; ++k) o += s_part[nth][k][lane];
   store4(out + lane * 4, o * (total == 0.f ? 0.f : 1.f / total));
 }
+
+// Whether codes pass the caches: a call that may read more than the 256 MB of the memory-side
+// cache finds nothing of it there the next time.
+inline bool streams(const seedlm_qcache_attend_args& a, int cap) {
+  const seedlm_qcache_t& c = a.cache;
+  const int64_t row = c.head_dim * c.bits / 8 + 4 * (c.head_dim / c.group);
+  return !a.rows && c.head_dim > 64 && (int64_t)a.queries * cap * c.kv_heads * 2 * row > (int64_t)256 << 20;
+}
+
+// Joins of more queries and heads than this take a wave each.
+constexpr int64_t kManyJoins = 2048;
 
 template <int D, int BITS, int NG, bool WIDE>
 int run_groups(const Args& p, hipStream_t s) {
   const seedlm_qcache_attend_args& a = p.a;
   const bool split = p.slots > 0;
-  hipLaunchKernelGGL((qcache_attend_kernel<D, BITS, NG, WIDE>),
-                     dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries), dim3(kThreads),
-                     (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
-  if (split)
-    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE>), dim3(a.heads, a.queries),
+  const auto kernel = streams(a, p.cap) ? qcache_attend_kernel<D, BITS, NG, WIDE, (D > 64)>
+                                        : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
+  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries),
+                     dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
+  if (split && (int64_t)a.heads * a.queries > kManyJoins)
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
+                       dim3(kThreads), 0, s, p);
+  else if (split)
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kThreads>), dim3(a.heads, a.queries),
                        dim3(kThreads), 0, s, p);
   return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
 }
