@@ -21,6 +21,44 @@ __device__ inline int slot_of(int u, int units, int slots) {
   return (int)(x / (uint32_t)units);
 }
 
+// The same with runs of several lengths: GENS workgroups of a compute unit run side by
+// side, and those that started first get the larger part of its loads, so of GENS equal
+// parts of the slots (workgroups start in the order of their numbers) each has longer
+// runs than the next.  Where units are few all runs are even.
+template <int GENS>
+struct Runs {
+  int units, slots, per;  // per: slots of a generation, the last one's but at least
+
+  __device__ Runs(int most, int u) : units(u), slots(min(most, u)) {
+    per = GENS > 1 && units >= 3 * slots ? slots / GENS : slots;
+  }
+  __device__ static constexpr int weight(int gen) {
+    return GENS == 1 ? 1 : (GENS == 2 ? 3 - gen : 4 - gen);  // 3 : 2, 4 : 3 : 2
+  }
+  // The weights of the slots before `slot`.
+  __device__ int before(int slot) const {
+    int sum = 0;
+#pragma unroll
+    for (int g = 0; g < GENS; ++g) {
+      const int first = g * per, n = g + 1 < GENS ? min(slot - first, per) : slot - first;
+      if (n > 0) sum += n * weight(g);
+    }
+    return sum;
+  }
+  __device__ int begin(int slot) const { return slot_begin(before(slot), units, before(slots)); }
+  __device__ int slot_of(int u) const {
+    int x = seedlm::slot_of(u, units, before(slots)), slot = 0;
+#pragma unroll
+    for (int g = 0; g < GENS; ++g) {
+      const bool last = g + 1 == GENS || x < per * weight(g);
+      slot += last ? x / weight(g) : per;
+      if (last) break;
+      x -= per * weight(g);
+    }
+    return min(slot, slots - 1);
+  }
+};
+
 // Inclusive sums of units_of(0), ..., units_of(n - 1) into ends[0..n), by all
 // THREADS threads, each taking consecutive numbers.
 template <int THREADS, typename F>

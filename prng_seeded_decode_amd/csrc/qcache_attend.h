@@ -228,6 +228,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
   using R = Row<D, BITS>;
   constexpr int kSteps = R::kSteps, kAccs = R::kAccs, KD = R::KD, VD = R::VD;
   constexpr int kStride = D + 4;  // LDS row stride (floats)
+  constexpr int kGens = waves_per_simd(D, BITS, NG, WIDE);
   __shared__ __align__(16) uint32_t s_off[kWaves][kTile];
   __shared__ __align__(16) uint32_t s_pair[kWaves][NG][2 * kTile];
   __shared__ float2 s_ml[kWaves][16];
@@ -258,10 +259,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         p.ends[b] = s_ends[b];
         p.firsts[b] = first;
       }
-    const int slots = min(p.slots, units);  // none is empty
-    if ((int)blockIdx.y >= slots) return;
-    run_begin = unit = slot_begin(blockIdx.y, units, slots);
-    unit_end = slot_begin(blockIdx.y + 1, units, slots);
+    const Runs<kGens> runs(p.slots, units);  // none is empty
+    if ((int)blockIdx.y >= runs.slots) return;
+    run_begin = unit = runs.begin(blockIdx.y);
+    unit_end = runs.begin(blockIdx.y + 1);
   } else {
     const int n = min(p.shared, a.queries - (int)blockIdx.y);
     if ((int)threadIdx.x < n) s_entry[threadIdx.x] = item_entry(p, blockIdx.y + threadIdx.x);
@@ -648,7 +649,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 // Joins the pieces of one query and head, and writes zeros for queries without any.
 // THREADS threads take a head, of 4 in a workgroup or alone; every wave forms the maximum
 // and the sum itself, and groups of D/4 lanes take the pieces in turn.
-template <int D, bool WIDE, int THREADS>
+template <int D, bool WIDE, int GENS, int THREADS>
 __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
   constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kHeads = kThreads / THREADS;
@@ -658,15 +659,15 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
   const int query = blockIdx.y, head = blockIdx.x * kHeads + nth;
   if (head >= a.heads) return;
   const int b = p.firsts[query];  // the item's first query
-  const int units = p.ends[a.queries - 1], slots = min(p.slots, units);
+  const Runs<GENS> runs(p.slots, p.ends[a.queries - 1]);
   const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
   // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
   // but the first, whose run may have begun before the item, they start the slot's run.
   int first_slot = 0, pieces = 0, skip = 0;
   if (u1 > u0) {
-    first_slot = slot_of(u0 + kItemUnits, units, slots);
-    pieces = slot_of(u1 - 1, units, slots) - first_slot + 1;
-    skip = slot_begin(first_slot, units, slots) < u0;
+    first_slot = runs.slot_of(u0 + kItemUnits);
+    pieces = runs.slot_of(u1 - 1) - first_slot + 1;
+    skip = runs.begin(first_slot) < u0;
   }
   if (pieces == 1) return;
   T* out = static_cast<T*>(a.out) + (int64_t)query * a.out_stride + (int64_t)head * D;
@@ -728,11 +729,12 @@ int run_groups(const Args& p, hipStream_t s) {
                                         : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
   hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries),
                      dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
+  constexpr int kGens = waves_per_simd(D, BITS, NG, WIDE);
   if (split && (int64_t)a.heads * a.queries > kManyJoins)
-    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kGens, 64>), dim3((a.heads + 3) / 4, a.queries),
                        dim3(kThreads), 0, s, p);
   else if (split)
-    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kThreads>), dim3(a.heads, a.queries),
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kGens, kThreads>), dim3(a.heads, a.queries),
                        dim3(kThreads), 0, s, p);
   return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
 }
