@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = kThreads / 4;  // rows of a workgroup
+constexpr int64_t kL2Bytes = 32 << 20;  // of all XCDs: larger outputs pass the caches
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
@@ -229,6 +230,7 @@ struct AppendArgs {
   Divisor page_size;
   int units;            // units of a head of q
   Divisor token_units;  // units of a token of q
+  bool stream;          // q passes the caches
 };
 
 // VEC: k, v and the angles in aligned fours.  N: pairs of a unit of q, 8 or 1.
@@ -262,8 +264,13 @@ __global__ __launch_bounds__(kThreads) void qcache_append_kernel(const AppendArg
         u.turn(x, y, co, si);
       }
     }
-    store<N>(dst + u.lo, x);
-    store<N>(dst + u.hi, y);
+    if (N == 8 && p.stream) {
+      store<N, true>(dst + u.lo, x);
+      store<N, true>(dst + u.hi, y);
+    } else {
+      store<N>(dst + u.lo, x);
+      store<N>(dst + u.hi, y);
+    }
     return;
   }
   constexpr int kI = D / 16;                 // codes of a unit
@@ -360,74 +367,100 @@ struct ReadArgs {
   Divisor page_size;
 };
 
-// WIDE: rows of the outputs are aligned to 16 bytes.  Then fp16 goes out by eights, so that
-// the four lanes write 64 bytes in a row: two neighbours exchange their units, and one takes
-// the codes of even i, the other those of odd i.
-template <int D, int BITS, int NG, bool WIDE, typename T>
+// How a row's elements are written: one by one, by aligned fours, or (rows aligned to 16
+// bytes) through LDS and past the caches, by 1 KB in a row where the four lanes of a row
+// alone write 32 or 64 bytes.
+enum Out { kEach, kFours, kStream };
+
+template <int D, int BITS, int NG, Out OUT, typename T>
 __global__ __launch_bounds__(kThreads) void qcache_read_kernel(const ReadArgs p) {
   constexpr int kI = D / 16, kUnitBytes = kI * BITS / 8, KD = kUnitBytes;
+  constexpr int kRowBytes = D * sizeof(T), kChunk = kRowBytes < 256 ? kRowBytes : 256;
+  constexpr int kChunkI = kChunk / (16 * (int)sizeof(T));  // i of a chunk
+  constexpr int kSteps = 16 * kChunk / 1024;               // stores of a wave's chunk
+  constexpr int kStride = kChunk + 32;                     // LDS row stride: two rows to 64 banks
+  __shared__ __align__(16) uint8_t s_out[OUT == kStream ? kThreads / 64 : 1][OUT == kStream ? 16 * kStride : 16];
   const seedlm_qcache_read_args& a = p.a;
   const seedlm_qcache_t& c = a.cache;
-  const int u = threadIdx.x & 3;
-  int token, row;
-  if (!p.split.at(threadIdx.x >> 2, blockIdx.y, c.kv_heads, &token, &row)) return;
-  const int64_t t = (int64_t)blockIdx.x * p.split.tokens + token;
-  if (t >= a.tokens) return;
-  const bool is_v = row >= c.kv_heads;
-  if (!(is_v ? a.v_out : a.k_out)) return;
-  const int h = is_v ? row - c.kv_heads : row, slot = a.slots[t];
+  const int u = threadIdx.x & 3, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // The output row of the workgroup's row r, or NULL.
+  int token = 0, row = 0;
+  auto out_of = [&](int r) -> T* {
+    if (!p.split.at(r, blockIdx.y, c.kv_heads, &token, &row)) return nullptr;
+    const int64_t t = (int64_t)blockIdx.x * p.split.tokens + token;
+    const bool is_v = row >= c.kv_heads;
+    T* out = static_cast<T*>(is_v ? a.v_out : a.k_out);
+    if (t >= a.tokens || !out) return nullptr;
+    return out + t * (is_v ? a.v_stride : a.k_stride) + (int64_t)(is_v ? row - c.kv_heads : row) * D;
+  };
+  T* out = out_of(threadIdx.x >> 2);
   uint32_t code[KD], pair[NG];
 #pragma unroll
   for (int k = 0; k < KD; ++k) code[k] = 0;
 #pragma unroll
   for (int n = 0; n < NG; ++n) pair[n] = 0;
-  if (slot >= 0 && slot < c.pages * c.page_size) {
-    const RowAt at(c, p.page_size, slot, h);
-    load_dwords(static_cast<const uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, code);
-    load_dwords(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
+  if (out) {
+    const int slot = a.slots[(int64_t)blockIdx.x * p.split.tokens + token];
+    if (slot >= 0 && slot < c.pages * c.page_size) {
+      const bool is_v = row >= c.kv_heads;
+      const RowAt at(c, p.page_size, slot, is_v ? row - c.kv_heads : row);
+      load_dwords(static_cast<const uint8_t*>(is_v ? c.v : c.k) + at.codes + u * 4 * KD, code);
+      load_dwords(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale) + at.pair, pair);
+    }
   }
-  T* out = (is_v ? static_cast<T*>(a.v_out) + t * a.v_stride
-                 : static_cast<T*>(a.k_out) + t * a.k_stride) + (int64_t)h * D;
+  [[maybe_unused]] T* to[kSteps];  // where the lane's 16 bytes of each store go
+  if constexpr (OUT == kStream) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int byte = k * 1024 + lane * 16;
+      to[k] = out_of(wave * 16 + byte / kChunk);
+      if (to[k]) to[k] += byte % kChunk / (int)sizeof(T);
+    }
+  }
   float s[NG], o[NG];
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
     s[n] = (float)__builtin_bit_cast(_Float16, (uint16_t)pair[n]);
     o[n] = (float)__builtin_bit_cast(_Float16, (uint16_t)(pair[n] >> 16));
   }
-  if constexpr (WIDE && sizeof(T) == 2) {
-    const int odd = u & 1;
-    uint32_t eight[2][KD];  // units 8 (u / 2) .. + 7, shifted to the codes of i % 2 == odd
+  auto elements = [&](int i, float (&x)[4]) {
+    const int n = i * NG / kI;
 #pragma unroll
-    for (int k = 0; k < KD; ++k) {
-      const uint32_t mine = code[k] >> (odd * BITS), other = in_row<kSwapOne>(code[k]) >> (odd * BITS);
-      eight[0][k] = odd ? other : mine;
-      eight[1][k] = odd ? mine : other;
-      if (BITS == 4) eight[0][k] &= 0x0F0F0F0Fu, eight[1][k] &= 0x0F0F0F0Fu;
+    for (int j = 0; j < 4; ++j) {
+      const int byte = j * kUnitBytes + i * BITS / 8;
+      uint32_t d = code[byte / 4];
+      if (BITS == 4) d = (i % 2 ? d >> 4 : d) & 0x0F0F0F0Fu;
+      x[j] = o[n] + s[n] * (float)(d >> (8 * (byte % 4)) & 0xFF);
     }
+  };
+  if constexpr (OUT == kStream) {
 #pragma unroll
-    for (int i = 0; i < kI; i += 2) {
-      const int n = i * NG / kI;
-      float x[8];
+    for (int i0 = 0; i0 < kI; i0 += kChunkI) {
+      uint8_t* mine = s_out[wave] + (lane >> 2) * kStride;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int byte = j % 4 * kUnitBytes + i * BITS / 8;
-        x[j] = o[n] + s[n] * (float)(eight[j / 4][byte / 4] >> (8 * (byte % 4)) & 0xFF);
+      for (int i = 0; i < kChunkI; ++i) {
+        float x[4];
+        elements(i0 + i, x);
+        store4<true>(reinterpret_cast<T*>(mine) + 16 * i + 4 * u, x);
       }
-      store<8>(out + 16 * (i + odd) + 8 * (u >> 1), x);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int byte = k * 1024 + lane * 16;
+        const v4u v = *reinterpret_cast<const v4u*>(s_out[wave] + byte / kChunk * kStride + byte % kChunk);
+        v4u* at = reinterpret_cast<v4u*>(to[k] + 16 * i0);
+        if (to[k]) __builtin_nontemporal_store(v, at);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-  } else {
+  } else if (out) {
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
-      const int n = i * NG / kI;
       float x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int byte = j * kUnitBytes + i * BITS / 8;
-        uint32_t d = code[byte / 4];
-        if (BITS == 4) d = (i % 2 ? d >> 4 : d) & 0x0F0F0F0Fu;
-        x[j] = o[n] + s[n] * (float)(d >> (8 * (byte % 4)) & 0xFF);
-      }
-      store4<WIDE>(out + 16 * i + 4 * u, x);
+      elements(i, x);
+      store4<OUT == kFours>(out + 16 * i + 4 * u, x);
     }
   }
 }
@@ -471,8 +504,9 @@ int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
   const bool vec = fours(a.k, a.k_stride, a.x_dtype) && fours(a.v, a.v_stride, a.x_dtype) &&
                    a.rot % 8 == 0 && aligned16(a.cos) && aligned16(a.sin);
   const bool wide = vec && wide_units(a);
-  AppendArgs p{a, RowSplit(a.cache.kv_heads), divisor((uint32_t)a.cache.page_size), wide ? D / 16 : D / 2, {}};
+  AppendArgs p{a, RowSplit(a.cache.kv_heads), divisor((uint32_t)a.cache.page_size), wide ? D / 16 : D / 2, {}, false};
   if (a.heads > 1024) p.split.tokens = 1;  // the grid's second dimension is short
+  p.stream = (int64_t)a.tokens * a.heads * D * (a.x_dtype == SEEDLM_F16 ? 2 : 4) > kL2Bytes;
   const int token_units = a.heads * p.units;
   p.token_units = divisor((uint32_t)token_units);
   const int q_passes = (p.split.tokens * token_units + kThreads - 1) / kThreads;
@@ -495,14 +529,20 @@ int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s) {
   const int64_t per = a.y_dtype == SEEDLM_F16 ? 8 : 4;  // elements of 16 bytes
   const bool wide = (!a.k_out || (a.k_stride % per == 0 && aligned16(a.k_out))) &&
                     (!a.v_out || (a.v_stride % per == 0 && aligned16(a.v_out)));
+  const int64_t bytes = (int64_t)a.tokens * a.cache.kv_heads * a.cache.head_dim *
+                        (a.y_dtype == SEEDLM_F16 ? 2 : 4) * ((a.k_out != nullptr) + (a.v_out != nullptr));
+  const bool stream = wide && bytes > kL2Bytes;
   const dim3 grid((a.tokens + p.split.tokens - 1) / p.split.tokens, p.split.passes);
   return with_row(a.cache, [&](auto d, auto bits, auto groups) {
     constexpr int kD = decltype(d)::value, kBits = decltype(bits)::value, kG = decltype(groups)::value;
     const bool f16 = a.y_dtype == SEEDLM_F16;
-    const auto kernel = wide ? (f16 ? qcache_read_kernel<kD, kBits, kG, true, __half>
-                                    : qcache_read_kernel<kD, kBits, kG, true, float>)
-                             : (f16 ? qcache_read_kernel<kD, kBits, kG, false, __half>
-                                    : qcache_read_kernel<kD, kBits, kG, false, float>);
+    const auto kernel =
+        stream ? (f16 ? qcache_read_kernel<kD, kBits, kG, kStream, __half>
+                      : qcache_read_kernel<kD, kBits, kG, kStream, float>)
+        : wide ? (f16 ? qcache_read_kernel<kD, kBits, kG, kFours, __half>
+                      : qcache_read_kernel<kD, kBits, kG, kFours, float>)
+               : (f16 ? qcache_read_kernel<kD, kBits, kG, kEach, __half>
+                      : qcache_read_kernel<kD, kBits, kG, kEach, float>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, p);
     return launched();
   });

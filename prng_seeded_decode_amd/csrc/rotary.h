@@ -27,17 +27,24 @@ __device__ void load(const T* p, float (&v)[N]) {
   }
 }
 
-template <int N, typename T>
+// STREAM: past the caches.
+template <int N, bool STREAM = false, typename T>
 __device__ void store(T* p, const float (&v)[N]) {
+  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+  [[maybe_unused]] auto put = [&](auto x, int i) {
+    v4u* at = reinterpret_cast<v4u*>(p) + i;
+    if (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(v4u, x), at);
+    else *at = __builtin_bit_cast(v4u, x);
+  };
   if constexpr (N == 8 && sizeof(T) == 2) {
     uint4 u;
     __half* h = reinterpret_cast<__half*>(&u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = __float2half_rn(v[i]);
-    *reinterpret_cast<uint4*>(p) = u;
+    put(u, 0);
   } else if constexpr (N == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    put(make_float4(v[0], v[1], v[2], v[3]), 0);
+    put(make_float4(v[4], v[5], v[6], v[7]), 1);
   } else {
     p[0] = (T)v[0];
   }

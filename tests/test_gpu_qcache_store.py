@@ -368,3 +368,62 @@ def test_another_stream_and_a_graph():
         at = x["slots"] // 16, x["slots"] % 16
         ref, _ = Q.values(want["v_cache"][at], want["v_scale"][at], 4)
         assert np.all(np.abs(v_out.double().cpu().numpy() - ref) <= R.rounding(ref, True) + R.U32 * np.abs(ref))
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("kv,dim,bits,groups", [(1, 64, 4, 2), (3, 64, 8, 1), (8, 128, 4, 4), (5, 128, 8, 1),
+                                                (40, 128, 4, 1), (2, 256, 4, 1), (7, 256, 8, 4)])
+def test_a_large_read_gives_what_small_ones_do(kv, dim, bits, groups, f16):
+    # outputs of more than 32 MB go out another way than small ones
+    import torch
+
+    import prng_seeded_decode_amd as S
+
+    tokens = (36 << 20) // (2 * kv * dim * (2 if f16 else 4)) + 3
+    x = make([11, kv, dim], 1, 1, kv, dim, 0, True, 16, 50, bits, dim // groups)
+    cache = [device({n: x[n] for n in CACHE}, True)[n] for n in CACHE]
+    slots = np.random.default_rng(1).integers(-20, 820, tokens).astype(np.int32)
+    slots = torch.from_numpy(slots).cuda()
+    dt = torch.float16 if f16 else torch.float32
+    both = torch.full((tokens, 2, kv, dim), 9.0, dtype=dt, device="cuda")
+    S.seedlm_qcache_read(*cache, slots, both[:, 0], both[:, 1])
+    part = 4001
+    for at in range(0, tokens, part):
+        n = min(part, tokens - at)
+        k, v = (torch.full((n, kv, dim), 8.0, dtype=dt, device="cuda") for _ in range(2))
+        S.seedlm_qcache_read(*cache, slots[at: at + n], k, v)
+        assert torch.equal(both[at: at + n, 0], k) and torch.equal(both[at: at + n, 1], v), at
+    one = torch.full((2 * tokens, kv, dim), 9.0, dtype=dt, device="cuda")
+    S.seedlm_qcache_read(*cache, slots.repeat(2), None, one)
+    assert torch.equal(one[:tokens], both[:, 1]) and torch.equal(one[tokens:], both[:, 1])
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("heads,kv,dim,rot,interleaved", [(40, 8, 128, 128, False), (9, 3, 256, 64, True),
+                                                          (32, 32, 64, 64, True), (3, 1, 128, 32, False)])
+def test_a_large_append_gives_what_small_ones_do(heads, kv, dim, rot, interleaved, f16):
+    # q of more than 32 MB goes out another way than small ones
+    import torch
+
+    import prng_seeded_decode_amd as S
+
+    tokens = (33 << 20) // (heads * dim * (2 if f16 else 4)) + 3
+    size = 16
+    x = make([12, heads, dim], 5, heads, kv, dim, rot, f16, size, tokens // size + 1, 4, dim // 2)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    d = device(x, True)
+    for k, h in (("q", heads), ("k", kv), ("v", kv)):
+        d[k] = torch.randn((tokens, h, dim), generator=g, device="cuda").to(d[k].dtype)
+    d["positions"] = torch.randint(-1, 98, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    d["slots"] = torch.randperm((tokens // size + 1) * size, generator=g, device="cuda")[:tokens].int()
+    results = []
+    for part in (tokens, 777):
+        cache = [d[n].clone() for n in CACHE]
+        q_out = torch.full_like(d["q"], 7.0)
+        for at in range(0, tokens, part):
+            e = {k: d[k][at: at + part] for k in ("q", "k", "v", "positions", "slots")}
+            S.seedlm_qcache_append(e["q"], e["k"], e["v"], d["cos"], d["sin"], e["positions"],
+                                   e["slots"], q_out[at: at + part], *cache, interleaved=interleaved)
+        results.append([q_out, *cache[:2], *(t.view(torch.int16) for t in cache[2:])])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
