@@ -86,6 +86,19 @@ __device__ void sum_units(int n, int32_t* ends, F units_of) {
   __syncthreads();
 }
 
+// x plus those of all lower lanes of the wave.
+__device__ inline int wave_sums(int x) {
+#define SEEDLM_ADD_DPP(ctrl, rows) x += __builtin_amdgcn_update_dpp(0, x, ctrl, rows, 0xF, false)
+  SEEDLM_ADD_DPP(0x111, 0xF);  // the lane 1, 2, 4 and 8 before in the same 16
+  SEEDLM_ADD_DPP(0x112, 0xF);
+  SEEDLM_ADD_DPP(0x114, 0xF);
+  SEEDLM_ADD_DPP(0x118, 0xF);
+  SEEDLM_ADD_DPP(0x142, 0xA);  // the last lane of the 16 before, into the second and fourth 16
+  SEEDLM_ADD_DPP(0x143, 0xC);  // the last lane of the first half, into the second
+#undef SEEDLM_ADD_DPP
+  return x;
+}
+
 // The first request whose inclusive sum exceeds u.
 __device__ inline int request_of(const int32_t* ends, int n, int u) {
   int lo = 0, hi = n - 1;

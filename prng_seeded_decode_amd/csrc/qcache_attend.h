@@ -68,8 +68,8 @@ struct Args {
   uint32_t page_unit, token_unit;  // strides of codes in units of 16 bytes
   uint32_t page_pair, token_pair;  // strides of pairs in rows of pairs
   Divisor page_size;
-  int32_t* ends;    // [queries] inclusive sums of units, for the join
-  int32_t* firsts;  // [queries] the first query of each one's item, for the join
+  uint32_t per_head;  // 2^16 / group, rounded up
+  int4* joins;    // [queries] see join_of
   float2* ml;     // [2 * slots][kv_heads * qtiles][16] maximum (log2) and sum
   float* acc;     // [2 * slots][kv_heads * qtiles][16][D]
 };
@@ -98,6 +98,17 @@ __device__ inline int2 item_of(const int32_t* e, int n) {
 
 // Units of an item in the split.
 __device__ inline int units_of(int len) { return len > 0 ? kItemUnits + (len + kUnit - 1) / kUnit : 0; }
+
+// What the join has to know of the queries of the item of units [u0, u1) that starts with
+// query `first`: that query, the first slot of its tokens, its pieces, and which of the two
+// of that slot its first piece is.  The pieces lie in consecutive slots: in each but the
+// first, whose run may have begun before the item, they start the slot's run.
+template <int GENS>
+__device__ int4 join_of(const Runs<GENS>& runs, int first, int u0, int u1) {
+  if (u1 == u0) return make_int4(first, 0, 0, 0);
+  const int slot = runs.slot_of(u0 + kItemUnits);
+  return make_int4(first, slot, runs.slot_of(u1 - 1) - slot + 1, runs.begin(slot) < u0);
+}
 
 __device__ inline half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
 __device__ inline half2v as_half2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
@@ -242,28 +253,42 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
   const int heads = min(16, p.group - qt * 16);  // of a query in this tile
   const int head0 = hk * p.group + qt * 16;
 
+  // The inclusive sums of the items' units, then the entries.  Up to 64 queries that share
+  // nothing are a lane each: every wave forms and writes the sums itself (all write the
+  // same numbers, so none waits for another).
+  const bool few = p.shared == 1 && a.queries <= 64;
   int unit = 0, unit_end = 1, run_begin = 0;
   int32_t* s_entry = s_ends;
   if (p.slots > 0) {
     s_entry = s_ends + a.queries;
-    for (int b = threadIdx.x; b < a.queries; b += kThreads) s_entry[b] = item_entry(p, b);
-    __syncthreads();
-    sum_units<kThreads>(a.queries, s_ends, [&](int b) {
-      return s_entry[b] < 0 ? 0 : units_of(item_of(s_entry + b, a.queries - b).y);
-    });
-    const int units = s_ends[a.queries - 1];
-    if (blockIdx.x == 0 && blockIdx.y == 0)
+    int units;
+    if (few) {
+      const int len = lane < a.queries ? length_of(p, lane) : 0;
+      const int upto = wave_sums(units_of(len));
+      if (lane < a.queries) s_ends[lane] = upto, s_entry[lane] = len;
+      units = __builtin_amdgcn_readlane(upto, 63);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      for (int b = threadIdx.x; b < a.queries; b += kThreads) s_entry[b] = item_entry(p, b);
+      __syncthreads();
+      sum_units<kThreads>(a.queries, s_ends, [&](int b) {
+        return s_entry[b] < 0 ? 0 : units_of(item_of(s_entry + b, a.queries - b).y);
+      });
+      units = s_ends[a.queries - 1];
+    }
+    const Runs<kGens> runs(p.slots, units);  // none is empty
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
       for (int b = threadIdx.x; b < a.queries; b += kThreads) {
         int first = b;
         while (s_entry[first] < 0) --first;
-        p.ends[b] = s_ends[b];
-        p.firsts[b] = first;
+        p.joins[b] = join_of(runs, first, first > 0 ? s_ends[first - 1] : 0, s_ends[first]);
       }
-    const Runs<kGens> runs(p.slots, units);  // none is empty
+    }
     if ((int)blockIdx.y >= runs.slots) return;
     run_begin = unit = runs.begin(blockIdx.y);
     unit_end = runs.begin(blockIdx.y + 1);
-  } else {
+  } else if (p.shared > 1) {
     const int n = min(p.shared, a.queries - (int)blockIdx.y);
     if ((int)threadIdx.x < n) s_entry[threadIdx.x] = item_entry(p, blockIdx.y + threadIdx.x);
     __syncthreads();
@@ -276,7 +301,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     const bool starts_run = unit == run_begin;
     int2 item;
     if (p.slots > 0) {
-      first_query = request_of(s_ends, a.queries, unit);
+      first_query = few ? __ffsll(__ballot(lane >= a.queries || s_ends[lane] > unit)) - 1
+                        : request_of(s_ends, a.queries, unit);
       item = item_of(s_entry + first_query, a.queries - first_query);
       const int u0 = first_query > 0 ? s_ends[first_query - 1] : 0, u1 = s_ends[first_query];
       const int upto = min(u1, unit_end);
@@ -287,17 +313,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       unit = upto;
       if (begin >= end) continue;  // the run ends before the item's tokens do begin
     } else {
-      item = item_of(s_entry, min(p.shared, a.queries - (int)blockIdx.y));
+      item = p.shared > 1 ? item_of(s_entry, min(p.shared, a.queries - (int)blockIdx.y))
+                          : make_int2(1, length_of(p, blockIdx.y));
       end = item.y;
       unit = unit_end;
     }
-
-    // This lane's column: a query and a head; columns past the last repeat it.
-    const int columns = item.x * heads;
-    const int column = min(m, columns - 1);
-    const int query = first_query + column / heads, head = head0 + column % heads;
-    int length = s_entry[p.slots > 0 ? query : query - first_query];
-    length = length < 0 ? -1 - length : length;
 
     const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
     const uint8_t* vbase = static_cast<const uint8_t*>(c.v) + hk * c.head_stride + m * R::kUnitBytes;
@@ -321,9 +341,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     };
     struct Tile {
       uint32_t k[2][KD], v[8][VD], pair[NG];
-      uint32_t live;  // bit j: this lane's token j of the tile exists
-      bool ok;        // this lane's token exists
-      bool whole;     // all tokens exist
+      uint32_t live;  // bit i: token i exists (the same in all lanes)
     };
     // Requests the tile that was looked up, and looks up tile `next`.
     auto request = [&](Tile& t, int next) {
@@ -332,8 +350,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       const uint32_t row = ok ? (uint32_t)page * p.page_pair + (uint32_t)nth * p.token_pair : 0;
       if (lane < kTile) s_off[wave][lane] = ok ? off : kNoToken;
       look_up(next);
-      t.ok = ok;
-      t.whole = !__any(!ok);
+      t.live = (uint32_t)__ballot(ok);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       uint32_t koff[2] = {s_off[wave][m], s_off[wave][16 + m]};
@@ -344,15 +361,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       for (int j = 0; j < 8; ++j) voff[j] = o[j >> 2][j & 3];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      t.live = 0xFF;
-      if (!t.whole) {  // tokens that do not exist read token 0 of page 0 and are masked
+      if (t.live != ~0u) {  // tokens that do not exist read token 0 of page 0 and are masked
         rare();
-        t.live = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          t.live |= (voff[j] != kNoToken) << j;
-          voff[j] = voff[j] != kNoToken ? voff[j] : 0;
-        }
+        for (int j = 0; j < 8; ++j) voff[j] = voff[j] != kNoToken ? voff[j] : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) koff[h] = koff[h] != kNoToken ? koff[h] : 0;
       }
@@ -367,6 +379,17 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     if (tiles > 0) {
       look_up(0);
       request(even, 1);
+    }
+
+    // This lane's column: a query and a head; columns past the last repeat it.
+    const int columns = item.x * heads;
+    const int column = min(m, columns - 1);
+    const int nth_query = p.shared > 1 ? (int)(column * p.per_head >> 16) : 0;
+    const int query = first_query + nth_query, head = head0 + column - nth_query * heads;
+    int length = item.y;
+    if (p.shared > 1) {
+      length = s_entry[p.slots > 0 ? query : nth_query];
+      length = length < 0 ? -1 - length : length;
     }
 
     // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
@@ -464,11 +487,16 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       }
     }
 
-    float top = -INFINITY, base = -INFINITY;  // running maximum (log2), and with E added
+    float base = -INFINITY;  // running maximum (log2) with E added
     float sum = 0.f, osum[NG];  // this lane's share of the weights, and of them times offsets
     floatx4 acc[kAccs];
-    uint32_t largest = 0;  // exponent bits of the largest scale so far
-    float E = -14.f;
+    // exponent bits of the largest scale so far, and E with 2^E above it
+    uint32_t largest = 0;
+    auto exponent = [](uint32_t bits) {
+      const float e = (float)(int)(bits >> 10) - 14.f;
+      return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(e)));
+    };
+    float E = exponent(0);
 #pragma unroll
     for (int j = 0; j < NG; ++j) osum[j] = 0.f;
 #pragma unroll
@@ -479,7 +507,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       uint32_t e = 0;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        uint32_t so = t.ok ? t.pair[n] : 0;
+        uint32_t so = (t.live >> (lane & 31)) & 1 ? t.pair[n] : 0;
         const uint32_t es = so & 0x7C00u, eo = so & 0x7C000000u;
         if (es == 0x7C00u || eo == 0x7C000000u) so = 0x7E007E00u;
         else e = max(e, es);
@@ -521,8 +549,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         }
       }
       const int tile_first = first + i * kUnit;
-      const bool masked = !t.whole || __any(tile_first + kTile > length);
-      uint32_t on = t.live;
+      const bool masked = t.live != ~0u || __any(tile_first + kTile > length);
+      // bit j: this lane's token j exists and its column attends to it
+      uint32_t on = (t.live >> (4 * g) & 15) | (t.live >> (16 + 4 * g) & 15) << 4;
       if (masked) {
         rare();
 #pragma unroll
@@ -536,18 +565,17 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
       most = max_of_column(most) * sc;
       const bool grows = __any(lane >= kTile && e > largest);
-      if (grows) {
+      if (grows || __any(most + E > base)) {
         rare();
-        if (lane < kTile) e = 0;
+        if (grows) {
+          if (lane < kTile) e = 0;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) e = max(e, (uint32_t)__shfl_xor((int)e, d));
-        largest = max(largest, e);
-        E = (float)(int)(largest >> 10) - 14.f;
-      }
-      if (grows || __any(most > top)) {
-        rare();
-        top = fmaxf(top, most);
-        const float up = top + E;
+          for (int d = 1; d < 64; d <<= 1) e = max(e, (uint32_t)__shfl_xor((int)e, d));
+          largest = (uint32_t)__builtin_amdgcn_readfirstlane((int)e);
+        }
+        const float was = E;
+        E = exponent(largest);
+        const float up = fmaxf(base + (E - was), most + E);
         const float shrink = up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up);
         base = up;
         sum *= shrink;
@@ -632,8 +660,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         o += f * *reinterpret_cast<const floatx4*>(&s_acc[w][h][d]);
       }
       if (whole) {
-        T* out = static_cast<T*>(a.out) + (int64_t)(first_query + h / heads) * a.out_stride +
-                 (int64_t)(head0 + h % heads) * D + d;
+        T* out = static_cast<T*>(a.out) + (int64_t)(first_query + (p.shared > 1 ? h / heads : 0)) * a.out_stride +
+                 (int64_t)(head0 + (p.shared > 1 ? h % heads : h)) * D + d;
         store4(out, o * (total == 0.f ? 0.f : 1.f / total));
       } else {
         const int64_t at =
@@ -649,7 +677,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 // Joins the pieces of one query and head, and writes zeros for queries without any.
 // THREADS threads take a head, of 4 in a workgroup or alone; every wave forms the maximum
 // and the sum itself, and groups of D/4 lanes take the pieces in turn.
-template <int D, bool WIDE, int GENS, int THREADS>
+template <int D, bool WIDE, int THREADS>
 __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
   constexpr int kLanes = D / 4, kGroups = THREADS / kLanes, kHeads = kThreads / THREADS;
@@ -658,23 +686,14 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
   const int thread = threadIdx.x % THREADS, nth = threadIdx.x / THREADS;
   const int query = blockIdx.y, head = blockIdx.x * kHeads + nth;
   if (head >= a.heads) return;
-  const int b = p.firsts[query];  // the item's first query
-  const Runs<GENS> runs(p.slots, p.ends[a.queries - 1]);
-  const int u0 = b > 0 ? p.ends[b - 1] : 0, u1 = p.ends[b];
-  // Its pieces lie in the slots first_slot .. first_slot + pieces - 1: in each
-  // but the first, whose run may have begun before the item, they start the slot's run.
-  int first_slot = 0, pieces = 0, skip = 0;
-  if (u1 > u0) {
-    first_slot = runs.slot_of(u0 + kItemUnits);
-    pieces = runs.slot_of(u1 - 1) - first_slot + 1;
-    skip = runs.begin(first_slot) < u0;
-  }
+  const int4 join = p.joins[query];
+  const int first_slot = join.y, pieces = join.z, skip = join.w;
   if (pieces == 1) return;
   T* out = static_cast<T*>(a.out) + (int64_t)query * a.out_stride + (int64_t)head * D;
   const int lane = thread % kLanes, group = thread / kLanes;
   const int in_group = head % p.group, heads = min(16, p.group - in_group / 16 * 16);
   const int block = head / p.group * p.qtiles + in_group / 16;
-  const int column = (query - b) * heads + in_group % 16;
+  const int column = (query - join.x) * heads + in_group % 16;
   const int blocks = a.cache.kv_heads * p.qtiles;
   auto partial = [&](int s) {
     return ((int64_t)(2 * (first_slot + s) + (s == 0 ? skip : 0)) * blocks + block) * 16 + column;
@@ -729,12 +748,11 @@ int run_groups(const Args& p, hipStream_t s) {
                                         : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
   hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries),
                      dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
-  constexpr int kGens = waves_per_simd(D, BITS, NG, WIDE);
   if (split && (int64_t)a.heads * a.queries > kManyJoins)
-    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kGens, 64>), dim3((a.heads + 3) / 4, a.queries),
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
                        dim3(kThreads), 0, s, p);
   else if (split)
-    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kGens, kThreads>), dim3(a.heads, a.queries),
+    hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, kThreads>), dim3(a.heads, a.queries),
                        dim3(kThreads), 0, s, p);
   return hipGetLastError() == hipSuccess ? SEEDLM_OK : SEEDLM_E_DEVICE;
 }

@@ -34,7 +34,7 @@ int slots_of(const seedlm_qcache_attend_args& a) {
 }
 
 struct Scratch {
-  size_t ends, ml, acc;  // byte offsets and the total size
+  size_t joins, ml, acc;  // byte offsets and the total size
   size_t bytes;
 };
 
@@ -42,8 +42,8 @@ Scratch scratch_of(const seedlm_qcache_attend_args& a) {
   const size_t n = (size_t)2 * slots_of(a) * a.cache.kv_heads * qtiles_of(a) * 16;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Scratch r;
-  r.ends = 0;
-  r.ml = up((size_t)2 * a.queries * sizeof(int32_t));
+  r.joins = 0;
+  r.ml = up((size_t)a.queries * sizeof(int4));
   r.acc = r.ml + up(n * sizeof(float2));
   r.bytes = n == 0 ? 0 : r.acc + n * a.cache.head_dim * sizeof(float);
   return r;
@@ -68,11 +68,11 @@ int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipS
   p.page_pair = (uint32_t)(c.scale_page_stride / groups);
   p.token_pair = (uint32_t)(c.scale_token_stride / groups);
   p.page_size = divisor((uint32_t)c.page_size);
+  p.per_head = (uint32_t)((65536 + p.group - 1) / p.group);
   const Scratch r = scratch_of(a);
   char* base = static_cast<char*>(scratch);
   if (base) {
-    p.ends = reinterpret_cast<int32_t*>(base + r.ends);
-    p.firsts = p.ends + a.queries;
+    p.joins = reinterpret_cast<int4*>(base + r.joins);
     p.ml = reinterpret_cast<float2*>(base + r.ml);
     p.acc = reinterpret_cast<float*>(base + r.acc);
   }
