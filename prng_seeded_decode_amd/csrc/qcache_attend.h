@@ -502,6 +502,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
     for (int i = 0; i < kAccs; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 
+    // Products of half a pair are fused sums with a zero that the compiler does not see: one
+    // mixed-precision instruction in the place of a conversion and a product.
+    float zero;
+    asm("s_mov_b32 %0, 0" : "=s"(zero));
     auto compute = [&](const Tile& t, int i) {
       // Pairs: none of a token that does not exist, NaN for what is not finite.
       uint32_t e = 0;
@@ -543,8 +547,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
           for (int j = 0; j < 4; ++j) {
             const half2v so = as_half2(kp[4 * h + j]);
             float& y = x[4 * h + j];
-            y = n == 0 ? (float)so[1] * qsum[n] : y + (float)so[1] * qsum[n];
-            y += (float)so[0] * s[j];
+            y = fmaf((float)so[1], qsum[n], n == 0 ? zero : y);
+            y = fmaf((float)so[0], s[j], y);
           }
         }
       }
@@ -602,12 +606,13 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const half2v a0 = as_half2(vp[2 * w]), a1 = as_half2(vp[2 * w + 1]);
-          osum[n] += x[2 * w] * (float)a0[1];
-          osum[n] += x[2 * w + 1] * (float)a1[1];
-          const float w0 = x[2 * w] * (float)a0[0], w1 = x[2 * w + 1] * (float)a1[0];
-          const auto h = __builtin_amdgcn_cvt_pkrtz(w0, w1);
+          osum[n] = fmaf((float)a0[1], x[2 * w], osum[n]);
+          osum[n] = fmaf((float)a1[1], x[2 * w + 1], osum[n]);
+          const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf((float)a0[0], x[2 * w], zero),
+                                                    fmaf((float)a1[0], x[2 * w + 1], zero));
           ph[w] = __builtin_bit_cast(uint32_t, h);
-          pl[w] = pack_rtz(w0 - (float)h[0], w1 - (float)h[1]);
+          pl[w] = pack_rtz(fmaf((float)a0[0], x[2 * w], -(float)h[0]),
+                           fmaf((float)a1[0], x[2 * w + 1], -(float)h[1]));
         }
 #pragma unroll
         for (int k = n * kAccs / NG; k < (n + 1) * kAccs / NG; ++k) {
