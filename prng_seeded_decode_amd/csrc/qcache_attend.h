@@ -63,7 +63,7 @@ struct Args {
   int group;    // query heads per cache head
   int qtiles;   // ceil(group / 16)
   int shared;   // queries of an item at most
-  int slots;    // runs of units; 0: one workgroup per item
+  int slots;    // runs of units; 0: one workgroup per `shared` queries
   int cap;      // largest length: min(max_len, max_pages * page_size)
   uint32_t page_unit, token_unit;  // strides of codes in units of 16 bytes
   uint32_t page_pair, token_pair;  // strides of pairs in rows of pairs
@@ -288,11 +288,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     if ((int)blockIdx.y >= runs.slots) return;
     run_begin = unit = runs.begin(blockIdx.y);
     unit_end = runs.begin(blockIdx.y + 1);
-  } else if (p.shared > 1) {
-    const int n = min(p.shared, a.queries - (int)blockIdx.y);
-    if ((int)threadIdx.x < n) s_entry[threadIdx.x] = item_entry(p, blockIdx.y + threadIdx.x);
+  } else if (p.shared > 1) {  // `shared` queries, which are an item or several
+    unit_end = min(p.shared, a.queries - (int)blockIdx.y * p.shared);
+    if ((int)threadIdx.x < unit_end)
+      s_entry[threadIdx.x] = item_entry(p, blockIdx.y * p.shared + threadIdx.x);
     __syncthreads();
-    if (s_entry[0] < 0) return;
   }
   while (unit < unit_end) {
     // The next item of the run and the tokens of it that lie in the run.
@@ -313,10 +313,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       unit = upto;
       if (begin >= end) continue;  // the run ends before the item's tokens do begin
     } else {
-      item = p.shared > 1 ? item_of(s_entry, min(p.shared, a.queries - (int)blockIdx.y))
-                          : make_int2(1, length_of(p, blockIdx.y));
+      first_query = blockIdx.y * p.shared + unit;
+      item = p.shared > 1 ? item_of(s_entry + unit, unit_end - unit)
+                          : make_int2(1, length_of(p, first_query));
       end = item.y;
-      unit = unit_end;
+      unit += item.x;
     }
 
     const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
@@ -388,7 +389,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     const int query = first_query + nth_query, head = head0 + column - nth_query * heads;
     int length = item.y;
     if (p.shared > 1) {
-      length = s_entry[p.slots > 0 ? query : nth_query];
+      length = s_entry[p.slots > 0 ? query : query - blockIdx.y * p.shared];
       length = length < 0 ? -1 - length : length;
     }
 
@@ -751,8 +752,8 @@ int run_groups(const Args& p, hipStream_t s) {
   const bool split = p.slots > 0;
   const auto kernel = streams(a, p.cap) ? qcache_attend_kernel<D, BITS, NG, WIDE, (D > 64)>
                                         : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
-  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, split ? p.slots : a.queries),
-                     dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
+  const int rows = split ? p.slots : (a.queries + p.shared - 1) / p.shared;
+  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, rows), dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
   if (split && (int64_t)a.heads * a.queries > kManyJoins)
     hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
                        dim3(kThreads), 0, s, p);

@@ -1,4 +1,6 @@
 // Launches of seedlm_qcache_attend; the kernels and how they work are in qcache_attend.h.
+#include <algorithm>
+
 #include "qcache_attend.h"
 
 namespace seedlm {
@@ -15,11 +17,32 @@ int cap_of(const seedlm_qcache_attend_args& a) {
 int group_of(const seedlm_qcache_attend_args& a) { return a.heads / a.cache.kv_heads; }
 int qtiles_of(const seedlm_qcache_attend_args& a) { return (group_of(a) + 15) / 16; }
 
-// Whether items are the workgroups.
+// Queries of an item at most: as many as fill the 16 columns, where rows can repeat.
+int shared_of(const seedlm_qcache_attend_args& a) {
+  return a.rows && group_of(a) < 16 ? 16 / group_of(a) : 1;
+}
+
+// Whether items are the workgroups: then an item's steps of kUnit tokens follow one
+// another, but the sums, the partials and the second launch (4 to 5 us) fall away.  That
+// pays up to so many steps, and up to twice as many where items fill half the chip.  Time
+// of a call, unsplit against split, lengths alike: one request of 8 cache heads and 128
+// dimensions, 4 bits, 8.4 and 10.1 us at 512 tokens, 10.1 and 10.1 at 768, 11.9 and 10.1
+// at 1024; 16 requests 12.6 and 13.9 at 1024, 16.3 and 16.8 at 1536, 19.9 and 17.5 at
+// 2048; 4 of 2 heads and 256 dimensions, 8 bits, 11.8 and 12.9 at 384, 13.2 and 13.0 at
+// 512; 8 of 32 heads and 64 dimensions, 8 bits, fp32, 11.5 and 16.0 at 1024, 17.8 and 20.3
+// at 2048, and 17.5 and 16.5 where they are ragged up to 2047.  With two workgroups for
+// every compute unit runs of even length gain nothing until lengths differ much: 64
+// requests 31.6 and 38.9 at 2048.  Items of several queries are as long as their
+// neighbours: 128 queries of one request of 2048 tokens (256 workgroups) 21.5 and 25.6,
+// 512 of 2048 46.6 and 56.5, 512 of 8192 159 and 164.
 bool unsplit(const seedlm_qcache_attend_args& a) {
-  const int64_t workgroups = (int64_t)a.queries * a.cache.kv_heads * qtiles_of(a);
-  int steps = 4 * 128 / a.cache.head_dim;
-  if (2 * workgroups >= device_cu_count() && steps < 8) steps *= 2;
+  const int64_t items = (a.queries + shared_of(a) - 1) / shared_of(a);
+  const int64_t workgroups = items * a.cache.kv_heads * qtiles_of(a);
+  int steps = a.cache.head_dim == 64 ? 7 : (a.cache.head_dim == 128 ? 6 : 4);
+  const int cus = device_cu_count();
+  if (2 * workgroups >= cus) steps *= 2;
+  if (workgroups >= 2 * cus) steps = std::max(steps, 16 * 128 / a.cache.head_dim);
+  if (shared_of(a) > 1 && workgroups >= cus) steps = workgroups >= 4 * cus ? 64 : 32;
   return cap_of(a) <= steps * kUnit;
 }
 
@@ -60,7 +83,7 @@ int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipS
   p.a = a;
   p.group = group_of(a);
   p.qtiles = qtiles_of(a);
-  p.shared = a.rows && p.group < 16 ? 16 / p.group : 1;
+  p.shared = shared_of(a);
   p.slots = slots_of(a);
   p.cap = cap_of(a);
   p.page_unit = (uint32_t)(c.page_stride / 16);
