@@ -1,12 +1,14 @@
 """One decoder layer's attention block, served from packed weights for a batch of requests.
 
     python examples/serve_attention_block.py [--config 3] [--requests 16] [--steps 64]
+        [--cache-bits 4]
 
 Every step: page tables, positions and slots from the requests' lengths
 (seedlm_cache_plan); the packed q, k and v projections (seedlm_gemv_many) with each request's
 adapter beside them (seedlm_lora_many); rotary positions and the cache write
 (seedlm_cache_append); attention over the pages (seedlm_cache_attend); the packed o projection
-and its adapters.  All buffers are made once and every call is marshalled once, so a step is a
+and its adapters.  With 4 or 8 cache bits keys and values are quantised as they are written and
+read as such (seedlm_qcache_append, seedlm_qcache_attend).  All buffers are made once and every call is marshalled once, so a step is a
 fixed list of launches and is captured into a HIP graph; lengths, pages and adapters only
 change on the GPU.  Weights, adapters and inputs are synthetic.
 """
@@ -32,10 +34,13 @@ class AttentionBlock:
     how many of the next rows each request takes: 1 for the next token, more for a piece of a
     prompt, 0 to wait, -1 to end.  `x` (fp16 [rows][hidden]) holds those rows one request
     after another, and `out` gets theirs; rows past the last one come out as zeros.
-    `adapter` (int32 [requests]) names each request's adapter, -1 for none."""
+    `adapter` (int32 [requests]) names each request's adapter, -1 for none.  The cache holds
+    fp16 (`cache_bits` 16), or codes of 4 or 8 bits with a scale and an offset for each of a
+    head's `groups` groups of elements."""
 
     def __init__(self, mats, heads, kv_heads, dim, requests, pages, rows=None, page_size=16,
-                 max_pages=64, adapters=4, rank=16, theta=500000.0, seed=0):
+                 max_pages=64, adapters=4, rank=16, theta=500000.0, seed=0, cache_bits=16,
+                 groups=1):
         g = torch.Generator(device="cuda").manual_seed(seed)
         f16 = dict(dtype=torch.float16, device="cuda")
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -60,8 +65,15 @@ class AttentionBlock:
         offsets = torch.zeros(requests + 1, **i32)
         self.rows, self.positions, self.slots, self.spans, self.row_adapter = (
             torch.zeros(n, **i32) for _ in range(5))
-        self.k_cache = torch.zeros((pages, page_size, kv_heads, dim), **f16)
-        self.v_cache = torch.zeros_like(self.k_cache)
+        if cache_bits == 16:
+            self.cache = [torch.zeros((pages, page_size, kv_heads, dim), **f16) for _ in range(2)]
+        else:  # a head's rows of a page in one run
+            pool = lambda row, dtype: torch.zeros((pages, kv_heads, page_size, *row), dtype=dtype,
+                                                  device="cuda").transpose(1, 2)
+            self.cache = [pool((dim * cache_bits // 8,), torch.uint8) for _ in range(2)]
+            self.cache += [pool((groups, 2), torch.float16) for _ in range(2)]
+        append, attend = ((S.CacheAppendCall, S.CacheAttendCall) if cache_bits == 16 else
+                          (S.QCacheAppendCall, S.QCacheAttendCall))
         inv = theta ** (-torch.arange(dim // 2, dtype=torch.float64, device="cuda") * 2 / dim)
         angle = torch.arange(max_pages * page_size, device="cuda")[:, None] * inv
         self.cos, self.sin = angle.cos().float(), angle.sin().float()
@@ -84,11 +96,11 @@ class AttentionBlock:
             S.GemvManyCall([q, k, v], [self.x] * 3, [self.q, self.k, self.v], batch=n),
             S.LoraCall([site(0, self.x, self.q), site(1, self.x, self.k), site(2, self.x, self.v)],
                        self.row_adapter, self.scales),
-            S.CacheAppendCall(heads_of(self.q, heads), heads_of(self.k, kv_heads),
-                              heads_of(self.v, kv_heads), self.cos, self.sin, self.positions,
-                              self.slots, heads_of(self.q, heads), self.k_cache, self.v_cache),
-            S.CacheAttendCall(heads_of(self.q, heads), self.k_cache, self.v_cache, self.table,
-                              self.spans, heads_of(self.mixed, heads), rows=self.rows),
+            append(heads_of(self.q, heads), heads_of(self.k, kv_heads), heads_of(self.v, kv_heads),
+                   self.cos, self.sin, self.positions, self.slots, heads_of(self.q, heads),
+                   *self.cache),
+            attend(heads_of(self.q, heads), *self.cache, self.table, self.spans,
+                   heads_of(self.mixed, heads), rows=self.rows),
             S.GemvManyCall([o], [self.mixed], [self.out], batch=n),
             S.LoraCall([site(3, self.mixed, self.out)], self.row_adapter, self.scales),
         ]
@@ -136,6 +148,7 @@ def main():
     ap.add_argument("--config", type=int, default=3, choices=(2, 3, 4), help="layer of workloads.CONFIGS")
     ap.add_argument("--requests", type=int, default=16)
     ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--cache-bits", type=int, default=16, choices=(4, 8, 16))
     args = ap.parse_args()
     if not 1 <= args.requests <= S.MAX_BATCH:
         ap.error(f"--requests must be 1 to {S.MAX_BATCH}")
@@ -143,7 +156,8 @@ def main():
     n = args.requests
     # one token a step, so a step's rows are the requests
     max_pages = -(-(args.steps + 2) // 16) + 1
-    block = AttentionBlock(mats, heads, kv_heads, dim, n, n * max_pages, max_pages=max_pages)
+    block = AttentionBlock(mats, heads, kv_heads, dim, n, n * max_pages, max_pages=max_pages,
+                           cache_bits=args.cache_bits)
     block.adapter.copy_(torch.arange(n) % 4)
     block.capture()
     block.step()

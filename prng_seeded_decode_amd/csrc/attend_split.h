@@ -10,12 +10,12 @@ namespace seedlm {
 // The first unit of a slot among `units`, and the slot of a unit: the largest i
 // with i * units / slots <= u, that is i * units < (u + 1) * slots.
 // (A 64-bit division takes half a microsecond, so it is left to the largest numbers.)
-__device__ inline int slot_begin(int slot, int units, int slots) {
+__host__ __device__ inline int slot_begin(int slot, int units, int slots) {
   const uint64_t x = (uint64_t)slot * (uint32_t)units;
   if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)slots);
   return (int)(x / (uint32_t)slots);
 }
-__device__ inline int slot_of(int u, int units, int slots) {
+__host__ __device__ inline int slot_of(int u, int units, int slots) {
   const uint64_t x = ((uint64_t)u + 1) * (uint32_t)slots - 1;
   if (x >> 32 == 0) return (int)((uint32_t)x / (uint32_t)units);
   return (int)(x / (uint32_t)units);
@@ -29,24 +29,24 @@ template <int GENS>
 struct Runs {
   int units, slots, per;  // per: slots of a generation, the last one's but at least
 
-  __device__ Runs(int most, int u) : units(u), slots(min(most, u)) {
+  __host__ __device__ Runs(int most, int u) : units(u), slots(most < u ? most : u) {
     per = GENS > 1 && units >= 3 * slots ? slots / GENS : slots;
   }
-  __device__ static constexpr int weight(int gen) {
+  __host__ __device__ static constexpr int weight(int gen) {
     return GENS == 1 ? 1 : (GENS == 2 ? 3 - gen : 4 - gen);  // 3 : 2, 4 : 3 : 2
   }
   // The weights of the slots before `slot`.
-  __device__ int before(int slot) const {
+  __host__ __device__ int before(int slot) const {
     int sum = 0;
 #pragma unroll
     for (int g = 0; g < GENS; ++g) {
-      const int first = g * per, n = g + 1 < GENS ? min(slot - first, per) : slot - first;
+      const int left = slot - g * per, n = g + 1 < GENS && left > per ? per : left;
       if (n > 0) sum += n * weight(g);
     }
     return sum;
   }
-  __device__ int begin(int slot) const { return slot_begin(before(slot), units, before(slots)); }
-  __device__ int slot_of(int u) const {
+  __host__ __device__ int begin(int slot) const { return slot_begin(before(slot), units, before(slots)); }
+  __host__ __device__ int slot_of(int u) const {
     int x = seedlm::slot_of(u, units, before(slots)), slot = 0;
 #pragma unroll
     for (int g = 0; g < GENS; ++g) {
@@ -55,7 +55,7 @@ struct Runs {
       if (last) break;
       x -= per * weight(g);
     }
-    return min(slot, slots - 1);
+    return slot < slots ? slot : slots - 1;
   }
 };
 

@@ -25,9 +25,10 @@ int check_qcache(const seedlm_qcache_t& c) {
       c.scale_token_stride % groups != 0 || c.scale_head_stride % groups != 0)
     return SEEDLM_E_UNSUPPORTED;
   // Rows are counted in 32 bits, by 16 bytes of codes and by a row's pairs (each
-  // stride's own bound first, so that the products fit 64 bits).
+  // stride's own bound first, so that the sum fits 64 bits).
+  auto fits = [](int64_t stride, int64_t n, int64_t most) { return n == 1 || stride <= most / (n - 1); };
   auto spans = [&](int64_t page, int64_t token, int64_t head, int64_t row, int64_t most) {
-    return page < most / c.pages && token < most / c.page_size && head < most / c.kv_heads &&
+    return fits(page, c.pages, most) && fits(token, c.page_size, most) && fits(head, c.kv_heads, most) &&
            page * (c.pages - 1) + token * (c.page_size - 1) + head * (c.kv_heads - 1) + row <= most;
   };
   if (!spans(c.page_stride, c.token_stride, c.head_stride, c.head_dim * c.bits / 8,
@@ -54,6 +55,16 @@ int check_read(const seedlm_qcache_read_args* a) {
   return SEEDLM_OK;
 }
 
+int check_qattend(const seedlm_qcache_attend_args* a) {
+  const int st = check_attend(a, check_qcache);
+  if (st != SEEDLM_OK) return st;
+  // The split's units, with what starting each query counts for, are 32-bit.
+  const int64_t room = (int64_t)a->max_pages * a->cache.page_size;
+  const int64_t cap = a->max_len < room ? a->max_len : room;
+  return (cap / 128 + 1 + kQcacheItemUnits) * a->queries > INT32_MAX ? SEEDLM_E_UNSUPPORTED
+                                                                      : SEEDLM_OK;
+}
+
 }  // namespace
 }  // namespace seedlm
 
@@ -74,7 +85,7 @@ int seedlm_qcache_read(const seedlm_qcache_read_args* args, void* stream) {
 }
 
 int seedlm_qcache_attend(const seedlm_qcache_attend_args* args, void* stream) {
-  int st = check_attend(args, check_qcache);
+  int st = check_qattend(args);
   if (st != SEEDLM_OK) return st;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   ScratchHold hold;
@@ -86,7 +97,7 @@ int seedlm_qcache_attend(const seedlm_qcache_attend_args* args, void* stream) {
 
 int seedlm_qcache_attend_scratch_bytes(const seedlm_qcache_attend_args* args, size_t* bytes) {
   if (!bytes) return SEEDLM_E_INVALID;
-  const int st = check_attend(args, check_qcache);
+  const int st = check_qattend(args);
   if (st != SEEDLM_OK) return st;
   *bytes = qcache_attend_scratch_bytes(*args);
   return SEEDLM_OK;

@@ -54,7 +54,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTile = 32;              // tokens of a wave's step
 constexpr int kUnit = kWaves * kTile;  // tokens of a workgroup's step
-constexpr int kItemUnits = 3;          // what starting an item counts for in the split
+constexpr int kItemUnits = kQcacheItemUnits;
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.44269504088896340736f;
 

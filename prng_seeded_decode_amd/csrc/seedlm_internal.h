@@ -175,6 +175,8 @@ size_t cache_attend_scratch_bytes(const seedlm_cache_attend_args& a);
 int launch_cache_attend(const seedlm_cache_attend_args& a, void* scratch, hipStream_t s);
 int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s);
 int launch_qcache_read(const seedlm_qcache_read_args& a, hipStream_t s);
+// What starting an item counts for in the split of qcache_attend.h, in units of tokens.
+constexpr int kQcacheItemUnits = 3;
 size_t qcache_attend_scratch_bytes(const seedlm_qcache_attend_args& a);
 int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipStream_t s);
 constexpr int kLoraGroup = 8;  // sites of one pair of launches

@@ -397,3 +397,60 @@ def test_attend_with_a_table_that_holds_more_than_32_bits_of_tokens():
     with pytest.raises(ValueError):
         run(y, max_len=-1)
     check(x, run(y, max_len=100))
+
+
+def widen(x, most, wild=-1):
+    """The same requests in a table of `most` pages a row."""
+    import torch
+
+    table = torch.full((x["table"].shape[0], most), wild, dtype=torch.int32, device="cuda")
+    table[:, : x["table"].shape[1]] = x["dtable"]
+    return dict(x, dtable=table)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("heads,kv,dim,size,groups,head_major", [
+    (8, 2, 128, 16, 1, False), (20, 1, 128, 48, 2, True), (4, 4, 128, 7, 4, False),
+    (4, 2, 256, 16, 2, True), (18, 1, 256, 100, 4, False)])
+def test_codes_past_the_caches(heads, kv, dim, size, groups, head_major, bits, f16):
+    # calls that may read more than 256 MB
+    lens = [0, 1, 33, 128, 129, 700, 3000, 255, 2049, 0]
+    row = dim * bits // 8 + 4 * groups
+    most = 2 ** 28 // (len(lens) * kv * 2 * row * size) + 2
+    x = widen(make([heads, dim, size, 7], lens, heads, kv, dim, size, f16, bits, groups, head_major), most,
+              wild=2 ** 31 - 1)
+    check(x, run(x))
+
+
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 200])
+@pytest.mark.parametrize("dim,groups", [(128, 1), (64, 2), (256, 1)])
+def test_split_of_any_number_of_requests(n, dim, groups):
+    # up to 64 queries are counted in registers, more in LDS; a wide table has them split
+    rng = np.random.default_rng([n, dim])
+    lens = [int(v) for v in np.exp(rng.uniform(0, np.log(900), n)).astype(int) * rng.integers(0, 2, n)]
+    lens[n // 2] = 1300
+    x = widen(make([n, dim], lens, 4, 2, dim, 16, True, 4, groups), 400)
+    check(x, run(x))
+
+
+@pytest.mark.parametrize("heads,kv", [(32, 2), (7, 7), (24, 8), (3, 1)])
+def test_rows_that_repeat_with_and_without_a_split(heads, kv):
+    # blocks of queries whose rows change inside, repeat after others, and end in padding
+    import torch
+
+    x = make([17, heads], [900, 40, 333], heads, kv, 64, 16, True, 4, 1)
+    rows = np.array([0] * 17 + [1] + [0] * 3 + [2] * 30 + [-1] * 4 + [1] * 9 + [2])
+    rng = np.random.default_rng(1)
+    lens = np.array([int(rng.integers(0, len(x["where"][r]))) if r >= 0 else 5 for r in rows])
+    q = torch.randn((len(rows), heads, 64), device="cuda").half()
+    host = q.cpu().numpy()
+    want = run_rows(x, q, rows, lens)
+    check(x, want, lens=lens, rows=rows, q=host)
+    got = run_rows(widen(x, 9000), q, rows, lens)
+    check(x, got, lens=lens, rows=rows, q=host)
+    # NaN behind every length of a row reaches none of its queries
+    page, row = x["where"][2][332]
+    x["cache"][3][page, row] = float("nan")
+    assert np.array_equal(run_rows(x, q, rows, lens), want)
+    assert np.array_equal(run_rows(widen(x, 9000), q, rows, lens), got)
