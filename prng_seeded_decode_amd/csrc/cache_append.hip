@@ -46,9 +46,14 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(const AppendArgs
     cache_at = page * a.cache.page_stride +
                (slot - page * a.cache.page_size) * a.cache.token_stride;
   }
-  const RotaryUnit<N> u(unit, a.rot, a.interleaved);
+  // The unit's two runs of N elements: the halves of N rotated pairs, or (as
+  // interleaved pairs and unrotated elements are) 2N in a row.
+  const int e0 = unit * 2 * N;
+  const bool rotated = e0 < a.rot;
+  const bool split = rotated && !a.interleaved;
+  const int lo = split ? unit * N : e0, hi = split ? lo + a.rot / 2 : e0 + N;
   float c[N], s[N];
-  if (u.rotated && turns) {
+  if (rotated && turns) {
     const int64_t at = (int64_t)pos * (a.rot / 2) + unit * N;
     load<N>(a.cos + at, c);
     load<N>(a.sin + at, s);
@@ -62,22 +67,44 @@ __global__ __launch_bounds__(kThreads) void cache_append_kernel(const AppendArgs
                       : (is_v ? static_cast<const T*>(a.v) + t * a.v_stride + hk * D
                               : static_cast<const T*>(a.k) + t * a.k_stride + hk * D);
   float x[N], y[N];
-  load<N>(src + u.lo, x);
-  load<N>(src + u.hi, y);
-  if (u.rotated && !is_v && turns) u.turn(x, y, c, s);
+  load<N>(src + lo, x);
+  load<N>(src + hi, y);
+  if (rotated && !is_v && turns) {
+    if (split) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u = x[i], w = y[i];
+        x[i] = u * c[i] - w * s[i];
+        y[i] = w * c[i] + u * s[i];
+      }
+    } else {
+      // elements 2i, 2i + 1 of the 2N in a row
+      float z[2 * N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = x[i], z[N + i] = y[i];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u = z[2 * i], w = z[2 * i + 1];
+        z[2 * i] = u * c[i] - w * s[i];
+        z[2 * i + 1] = w * c[i] + u * s[i];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = z[i], y[i] = z[N + i];
+    }
+  }
   if (is_q) {
     T* dst = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * D;
     if (!turns) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = y[i] = 0.f;
     }
-    store<N>(dst + u.lo, x);
-    store<N>(dst + u.hi, y);
+    store<N>(dst + lo, x);
+    store<N>(dst + hi, y);
   } else {
     __half* dst = static_cast<__half*>(is_v ? a.cache.v : a.cache.k) + cache_at +
                   hk * a.cache.head_stride;
-    store<N>(dst + u.lo, x);
-    store<N>(dst + u.hi, y);
+    store<N>(dst + lo, x);
+    store<N>(dst + hi, y);
   }
 }
 

@@ -1,4 +1,5 @@
-// Units of rotated elements, as both append kernels load, turn and store them.
+// Units of rotated elements: their loads and stores in both append kernels, and their
+// rotation in that of the quantised cache.
 #pragma once
 
 #include <hip/hip_fp16.h>
