@@ -297,11 +297,11 @@ SEEDLM_API int seedlm_qcache_read(const seedlm_qcache_read_args* args, void* str
  * seedlm_qcache_attend -- seedlm_cache_attend for a quantised cache.  The arguments
  * but `cache` are those of seedlm_cache_attend, and so are their bounds, lengths,
  * rows and queries of no tokens.
- * The codes enter the products as they are, exactly, and the pairs in fp32.  Scores,
+ * Codes and fp16 queries enter the products exactly, and the pairs in fp32.  Scores,
  * softmax statistics and sums are fp32; the softmax weights, times the values'
  * scales, enter the matrix cores as the sum of two fp16 numbers (22 bits), as do
- * fp32 queries, and fp16 queries exactly but for elements below 2^-20 of their row's
- * largest.  A group whose pair is not finite among the keys that a query attends to
+ * fp32 queries.  (8-bit codes of fp16 calls are small subnormal numbers there: where
+ * few tokens count, sums of them lose some 2^-21 of their terms' magnitudes.)  A group whose pair is not finite among the keys that a query attends to
  * makes its head's output NaN, among the values the elements of that group.  What
  * lies in the cache beyond a query's length does not reach its output.
  * Consecutive queries of one row share what they read of the cache.

@@ -6,10 +6,9 @@
 //   q . k_t     = sum_j (s_tj sum_{d in j} q_d c_td + o_tj sum_{d in j} q_d)
 //   sum_t p_t v_td = sum_t (p_t s_tj) c_td + sum_t p_t o_tj
 // so a group costs its pair's products and not a multiplication per element, and
-// nothing is rounded on the way.  A code in the low bits of an fp16 number is the
-// subnormal c 2^-24, which the matrix cores take exactly: a mask and at most a byte
-// permutation unpack two codes.  Bits 4 to 7 hold 16 c 2^-24; the query elements that
-// meet those are divided by 16, and so are the outputs that come of them.
+// no dequantised value is rounded.  A code in the low bits of an fp16 number is a
+// subnormal one: c 2^-24 of 8 bits, 16 c 2^-24 of 4 bits in the bits 4 to 7, so a byte
+// permutation, a mask and for every second code of 4 bits a shift unpack two codes.
 //
 // Split.  As in cache_attend.hip: the 128-token units of all items, one after another,
 // are cut into even runs, one per workgroup and cache head, and what is cut is joined by
@@ -30,6 +29,9 @@
 // Pairs pass through LDS, where 4 tokens' are one read.
 //
 // Precision.  p s enters the second product as the sum of two fp16 numbers (22 bits).
+// What subnormal codes cost the sums, and which calls avoid it, is at Row.  fp32 outputs
+// over 8 ragged requests err by 5.8e-7 of their norm, 32-bit sums of dequantised values
+// by 5.9e-7.
 // Values' scales may have any fp16 exponent, so the running maximum is taken of
 // x + E with 2^E above every scale so far: weights stay below 2^15.
 #pragma once
@@ -147,10 +149,23 @@ __device__ inline uint32_t pair_bytes(uint32_t a, uint32_t b, int n) {
   return __builtin_amdgcn_perm(b, a, 0x0C040C00u + 0x00010001u * n);
 }
 
-constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // codes c and 16 c of two bytes
+constexpr uint32_t kHigh = 0x00F000F0u;  // 16 c of two bytes' high codes
 
-template <int D, int BITS>
+template <int D, int BITS, bool WIDE>
 struct Row {
+  // What a code of 1 is in an operand.  The matrix instructions take a subnormal number as one
+  // of the smallest normal ones and line the products up by that, so a small code costs its
+  // sums low bits, the same way in all of them.  Codes of 4 bits are therefore all put where
+  // the high ones are, and those of fp32 calls are made normal numbers, at one more
+  // instruction for two codes.  (Weights of one token over others, the sums' relative errors:
+  // 4 bits at 2^-24 7e-7, of mean -6e-7, at 2^-20 1e-7 without a mean; normal 1e-7.)
+  static constexpr float kCode = (BITS == 4 ? 0x1p-20f : 0x1p-24f) * (WIDE ? 0x1p15f : 1.f);
+  __device__ static half8 operand(v4u r) {
+    if constexpr (!WIDE) return as_half8(r);
+    return as_half8(r) * (_Float16)0x1p15f;
+  }
+
+
   static constexpr int kBytes = D * BITS / 8;
   static constexpr int kUnitBytes = kBytes / 16;
   static constexpr int KD = kBytes / 16;                             // dwords of 4 units
@@ -174,9 +189,9 @@ struct Row {
         const int d = c / 4, n = c % 4;
         lo = pair_bytes(k[d], k[VD + d], n), hi = pair_bytes(k[2 * VD + d], k[3 * VD + d], n);
       }
-      r = v4u{lo & kLow, lo & kHigh, hi & kLow, hi & kHigh};
+      r = v4u{(lo << 4) & kHigh, lo & kHigh, (hi << 4) & kHigh, hi & kHigh};
     }
-    return as_half8(r);
+    return operand(r);
   }
 
   // The operand of code i from a unit of 8 tokens.
@@ -186,15 +201,17 @@ struct Row {
     for (int x = 0; x < 4; ++x) {
       const int byte = i * BITS / 8;
       const uint32_t b = pair_bytes(v[2 * x][byte / 4], v[2 * x + 1][byte / 4], byte % 4);
-      r[x] = BITS == 8 ? b : b & (i % 2 ? kHigh : kLow);
+      r[x] = BITS == 8 ? b : (i % 2 ? b : b << 4) & kHigh;
     }
-    return as_half8(r);
+    return operand(r);
   }
 
-  // The operand of keys() whose codes are all 1.
+  // The operand of keys() whose codes are all 1, divided by kCode: the offsets carry what its
+  // products lose into every score (6.8e-7 of their magnitudes' sum with subnormal 1s, nothing
+  // with 1s).
   __device__ static half8 ones() {
-    const uint32_t odd = BITS == 8 ? 0x00010001u : 0x00100010u;
-    return as_half8(v4u{0x00010001u, odd, 0x00010001u, odd});
+    const uint32_t one = 0x3C003C00u;
+    return as_half8(v4u{one, one, one, one});
   }
 };
 
@@ -236,7 +253,7 @@ template <int D, int BITS, int NG, bool WIDE, bool STREAM>
 __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void qcache_attend_kernel(
     const Args p) {
   using T = std::conditional_t<WIDE, float, __half>;
-  using R = Row<D, BITS>;
+  using R = Row<D, BITS, WIDE>;
   constexpr int kSteps = R::kSteps, kAccs = R::kAccs, KD = R::KD, VD = R::VD;
   constexpr int kStride = D + 4;  // LDS row stride (floats)
   constexpr int kGens = waves_per_simd(D, BITS, NG, WIDE);
@@ -396,7 +413,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     // Query operands of step s: elements 16 (2s) + 4g + (0..3) and 16 (2s + 1) + 4g +
     // (0..3), in the order of Row::keys.
     half8 qh[kSteps], ql[WIDE ? kSteps : 1];
-    float sc = a.scale * kLog2e * 0x1p24f;  // of products, to scores in powers of 2
+    float sc = a.scale * kLog2e * (1.f / R::kCode);  // of products, to scores in powers of 2
     float qsum[NG];  // of a group's elements, in the units of its products with codes
     {
       using Four = std::conditional_t<WIDE, floatx4, v2u>;
@@ -404,64 +421,29 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       Four raw[2 * kSteps];
 #pragma unroll
       for (int s = 0; s < 2 * kSteps; ++s) raw[s] = *reinterpret_cast<const Four*>(q + 16 * s);
-      // fp16 goes in as it is and divided by 16 where that keeps all bits that count: where
-      // the row's largest element is at least 2, so that what falls below fp16's normal
-      // numbers is rounded to 2^-22 of that.  Other rows, and fp32 ones, are multiplied by a power
-      // of two that puts their largest element into [2^9, 2^10).
-      bool as_is = false;
+      // fp16 goes in as it is.  fp32 rows are multiplied by a power of two that puts their
+      // largest element into [2^9, 2^10), and go in as the sum of two fp16 numbers.
       if constexpr (!WIDE) {
-        half2v most = {0, 0};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          qh[s] = as_half8(v4u{raw[2 * s][0], raw[2 * s + 1][0], raw[2 * s][1], raw[2 * s + 1][1]});
+      } else {
+        float most = 0.f;
 #pragma unroll
         for (int s = 0; s < 2 * kSteps; ++s)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w = raw[s][j];
-            most = __builtin_elementwise_max(most, as_half2(w & 0x7FFF7FFFu));
-          }
-        const float top = max_of_column(fmaxf((float)most[0], (float)most[1]));
-        as_is = BITS == 8 || !__any(!(top >= 2.f));
-        const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          uint32_t odd[2] = {raw[2 * s + 1][0], raw[2 * s + 1][1]};
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (BITS == 4) odd[j] = __builtin_bit_cast(uint32_t, as_half2(odd[j]) * sixteenth);
-          qh[s] = as_half8(v4u{raw[2 * s][0], odd[0], raw[2 * s][1], odd[1]});
-        }
-      }
-      if (!as_is) {
-        rare();
-        float f[kSteps][8], most = 0.f;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float x;
-              if constexpr (WIDE) {
-                x = raw[2 * s + h][j];
-              } else {
-                const uint32_t w = raw[2 * s + h][j / 2];
-                x = (float)as_half2(w)[j % 2];
-              }
-              f[s][(j / 2) * 4 + h * 2 + j % 2] = x;
-              most = fmaxf(most, fabsf(x));
-            }
-        }
+          for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(raw[s][j]));
         most = max_of_column(most);
         int e = 10;
         if (most > 0.f && most < INFINITY) (void)frexpf(most, &e);
-        const int up = 10 - e;
-        sc = ldexpf(a.scale * kLog2e, 24 - up);
+        sc = ldexpf(sc, e - 10);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float x = ldexpf(f[s][j], BITS == 4 && (j & 2) ? up - 4 : up);
+            const float x = ldexpf(raw[2 * s + (j >> 1 & 1)][(j >> 2) * 2 + (j & 1)], 10 - e);
             qh[s][j] = (_Float16)x;
-            if constexpr (WIDE) ql[s][j] = (_Float16)(x - (float)qh[s][j]);
+            ql[s][j] = (_Float16)(x - (float)qh[s][j]);
           }
       }
       // Scores times sc have to grow with the products: a negative scale turns the query, and
@@ -484,7 +466,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
           s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), qh[i], s, 0, 0, 0);
           if constexpr (WIDE) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(R::ones(), ql[i], s, 0, 0, 0);
         }
-        qsum[j] = s[0];
+        qsum[j] = s[0] * R::kCode;
       }
     }
 
@@ -649,7 +631,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
       for (int i = 0; i < kAccs; ++i)
         *reinterpret_cast<floatx4*>(&s_acc[wave][m][i * 16 + g * 4]) =
-            acc[i] * (BITS == 4 && i % 2 ? 0x1p20f : 0x1p24f) + osum[i * NG / kAccs];
+            acc[i] * (1.f / R::kCode) + osum[i * NG / kAccs];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < columns * (D / 4); e += kThreads) {

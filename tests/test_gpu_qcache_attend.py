@@ -454,3 +454,29 @@ def test_rows_that_repeat_with_and_without_a_split(heads, kv):
     x["cache"][3][page, row] = float("nan")
     assert np.array_equal(run_rows(x, q, rows, lens), want)
     assert np.array_equal(run_rows(widen(x, 9000), q, rows, lens), got)
+
+
+@pytest.mark.parametrize("bits,groups,dim", [(4, 1, 64), (4, 4, 128), (4, 2, 256), (8, 1, 64), (8, 2, 128)])
+def test_sums_of_fp32_calls_keep_their_low_bits(bits, groups, dim):
+    # The bounds element by element are of the worst case; errors on one side hide below them.
+    # So the root mean square over all outputs, relative to the terms' magnitudes: a weight is
+    # cut to 22 bits in two parts (2^-21), sums and products round 8 times at their size, and a
+    # score errs by 8 roundings of its terms' magnitudes, independently from token to token, so
+    # that 1 / sqrt(tokens that count) of it is left.
+    n = 1024
+    x = make([bits, groups, dim, 77], [n], 8, 8, dim, 64, False, bits, groups)
+    got = run(x)[0]
+    q = x["q"][0].astype(np.float64)
+    k, kmag, v, vmag = x["terms"][0]
+    scale = np.float64(np.float32(dim ** -0.5))
+    err, terms_, left = [], [], []
+    for h in range(8):
+        s = k[:, h] @ q[h] * scale
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        err.append(got[h] - w @ v[:, h])
+        terms_.append(w @ vmag[:, h])
+        left.append((kmag[:, h] @ np.abs(q[h])).max() * scale * np.sqrt((w ** 2).sum()))
+    size = np.sqrt(np.mean(np.square(terms_)))
+    bound = 2.0 ** -21 + 8 * Q.U32 + 8 * Q.U32 * max(left)
+    assert np.sqrt(np.mean(np.square(err))) <= bound * size
