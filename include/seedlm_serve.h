@@ -224,7 +224,7 @@ SEEDLM_API int seedlm_cache_attend_scratch_bytes(const seedlm_cache_attend_args*
  * four groups to a row.  The code pools are 16-byte aligned and their strides
  * multiples of 16; the pair pools are aligned to a row's pairs and their strides
  * are multiples of head_dim / group.  A code pool spans less than 2^36 bytes and a
- * pair pool less than 2^32 rows.
+ * pair pool less than 2^32 rows, and so does each stride times its number of steps.
  */
 typedef struct seedlm_qcache_t {
   void* k;

@@ -26,7 +26,7 @@ int check_qcache(const seedlm_qcache_t& c) {
     return SEEDLM_E_UNSUPPORTED;
   // Rows are counted in 32 bits, by 16 bytes of codes and by a row's pairs (each
   // stride's own bound first, so that the sum fits 64 bits).
-  auto fits = [](int64_t stride, int64_t n, int64_t most) { return n == 1 || stride <= most / (n - 1); };
+  auto fits = [](int64_t stride, int64_t n, int64_t most) { return stride <= (most - 1) / n; };
   auto spans = [&](int64_t page, int64_t token, int64_t head, int64_t row, int64_t most) {
     return fits(page, c.pages, most) && fits(token, c.page_size, most) && fits(head, c.kv_heads, most) &&
            page * (c.pages - 1) + token * (c.page_size - 1) + head * (c.kv_heads - 1) + row <= most;
