@@ -12,6 +12,13 @@
 // with its neighbours.  The other half of a rotated pair is loaded too (it is in the
 // caches) and not exchanged, so that any part of a head may turn.  q goes through the
 // units of rotary.h in workgroups of its own.
+//
+// Measured (medians, one MI355X): append of 4097 tokens, 32/32 heads of 128, 4 bits, a
+// group a row: 34.5 us; read of the same 21.6; read of 32771 tokens, two groups: 28.1 us
+// for 170 MB, 6.0 TB/s, the rate of a streaming read.  Small calls are a launch and a
+// chain of loads: append of 16 tokens 4.2, read of 300 tokens 3.2.  Dropped: a read with
+// four rows to a thread (47 us where this form had 43), an append with six waves to a
+// SIMD or four (46 and 38.3, five 34.5).
 #include <type_traits>
 
 #include "divisor.h"

@@ -32,8 +32,16 @@
 // What subnormal codes cost the sums, and which calls avoid it, is at Row.  fp32 outputs
 // over 8 ragged requests err by 5.8e-7 of their norm, 32-bit sums of dequantised values
 // by 5.9e-7.
-// Values' scales may have any fp16 exponent, so the running maximum is taken of
-// x + E with 2^E above every scale so far: weights stay below 2^15.
+//
+// Measured (medians, three inputs in turn; one MI355X).  One request of 131071 tokens, 64/8
+// heads of 128, 4 bits, 142 MB: 32.3 us and 5.2 of the join, 4.4 TB/s, where a streaming
+// read has 6.2; 64 ragged ones up to 16384, 32/8 heads: 116 to 128 and 5.2 (the inputs
+// between 97 and 147); 16 ragged ones up to 8192, 64/8 heads, two groups: 23.7 and 4.6.
+// Memory and the vector units bound them together: in 70% of the SIMDs' busy cycles a
+// vector instruction goes on (unpacking, the softmax of 16 columns), in a fifth or less a
+// matrix one.  Pieces of prompts (128 queries, four groups, 55 us) read little and spend as
+// large a share on vector instructions; 256 dimensions of 8 bits only a third, with one
+// wave per SIMD to cover the waits (18.6 us and 4.0 for 64 MB).
 #pragma once
 
 #include <hip/hip_fp16.h>
@@ -242,7 +250,7 @@ __device__ void load_codes(const uint8_t* p, uint32_t (&out)[N]) {
 }
 
 // Waves of the kernel per SIMD, and so workgroups per compute unit: what the registers
-// of each form allow.
+// of each form allow.  (One more of the 128-dimensional forms spills and is slower.)
 __host__ __device__ constexpr int waves_per_simd(int D, int bits, int groups, bool wide) {
   if (D == 256) return bits == 8 || wide || groups > 1 ? 1 : 2;
   return D == 128 && (bits == 8 || wide || groups > 1) ? 2 : 3;
@@ -717,26 +725,39 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
   store4(out + lane * 4, o * (total == 0.f ? 0.f : 1.f / total));
 }
 
-// Whether codes pass the caches: a call that may read more than the 256 MB of the memory-side
-// cache finds nothing of it there the next time.
+// Whether codes pass the caches: calls that read so much find little of it there the next
+// time, when the call has gone round other layers' caches.  Against caching, 16 requests
+// alike, three inputs in turn: 128 dimensions, 4 bits, 31.9 and 33.0 us at 120 MB, 64.5 and
+// 67.5 at 300, 175 and 179 at 900, 8 bits 30.9 and 32.1, 58.8 and 64.1, 154 and 169; 256, 4
+// bits, 64.4 and 67.2 at 300.  Below, all inputs may lie in the memory-side cache: 24.6
+// and 23.5 at 68 MB; the lengths are not known here, and ragged ones of half the bound lose
+// 2 to 4%.  64 dimensions of 8 bits gain as much (58.3 and 64.2 at 300), rows of
+// 32 bytes nothing (81.8 and 80.6), and rows of 256 bytes lose (39 and 34, 73 and 65, 187
+// and 169).
+constexpr bool may_stream(int row_bits) { return row_bits == 512 || row_bits == 1024; }
+
 inline bool streams(const seedlm_qcache_attend_args& a, int cap) {
   const seedlm_qcache_t& c = a.cache;
   const int64_t row = c.head_dim * c.bits / 8 + 4 * (c.head_dim / c.group);
-  return !a.rows && c.head_dim > 64 && (int64_t)a.queries * cap * c.kv_heads * 2 * row > (int64_t)256 << 20;
+  return !a.rows && may_stream(c.head_dim * c.bits) &&
+         (int64_t)a.queries * cap * c.kv_heads * 2 * row > (int64_t)110 << 20;
 }
 
-// Joins of more queries and heads than this take a wave each.
+// Joins of so many queries and heads take a wave each, fewer a workgroup, which reads the
+// many pieces of long requests faster.  Calls, waves against workgroups: 64 requests of 32
+// heads 50.5 and 51.7 us, 256 of 32 167 and 169; 16 of 64 22.0 and 21.7, one of 100000
+// tokens 34.3 and 31.4.
 constexpr int64_t kManyJoins = 2048;
 
 template <int D, int BITS, int NG, bool WIDE>
 int run_groups(const Args& p, hipStream_t s) {
   const seedlm_qcache_attend_args& a = p.a;
   const bool split = p.slots > 0;
-  const auto kernel = streams(a, p.cap) ? qcache_attend_kernel<D, BITS, NG, WIDE, (D > 64)>
+  const auto kernel = streams(a, p.cap) ? qcache_attend_kernel<D, BITS, NG, WIDE, may_stream(D * BITS)>
                                         : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
   const int rows = split ? p.slots : (a.queries + p.shared - 1) / p.shared;
   hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, rows), dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
-  if (split && (int64_t)a.heads * a.queries > kManyJoins)
+  if (split && (int64_t)a.heads * a.queries >= kManyJoins)
     hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
                        dim3(kThreads), 0, s, p);
   else if (split)

@@ -480,3 +480,16 @@ def test_sums_of_fp32_calls_keep_their_low_bits(bits, groups, dim):
     size = np.sqrt(np.mean(np.square(terms_)))
     bound = 2.0 ** -21 + 8 * Q.U32 + 8 * Q.U32 * max(left)
     assert np.sqrt(np.mean(np.square(err))) <= bound * size
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_the_most_queries_of_the_widest_heads_in_the_split_form(shared):
+    # the largest LDS of any call: the entries and sums of 4096 queries beside partials of 256
+    import torch
+
+    n = 4096
+    lens = np.random.default_rng(5).integers(0, 3, n)
+    lens[[7, 2000, 4095]] = 2300, 1, 1100
+    x = make([256, n, shared], list(lens), 2, 1, 256, 32, True, 4, 2)
+    rows = torch.arange(n, dtype=torch.int32, device="cuda") if shared else None
+    check(x, run(x, rows=rows))
