@@ -299,11 +299,14 @@ SEEDLM_API int seedlm_qcache_read(const seedlm_qcache_read_args* args, void* str
  * rows and queries of no tokens.
  * Codes and fp16 queries enter the products exactly, and the pairs in fp32.  Scores,
  * softmax statistics and sums are fp32; the softmax weights, times the values'
- * scales, enter the matrix cores as the sum of two fp16 numbers (22 bits), as do
- * fp32 queries.  (8-bit codes of fp16 calls are small subnormal numbers there: where
- * few tokens count, sums of them lose some 2^-21 of their terms' magnitudes.)  A group whose pair is not finite among the keys that a query attends to
- * makes its head's output NaN, among the values the elements of that group.  What
- * lies in the cache beyond a query's length does not reach its output.
+ * scales, enter the matrix cores as the sum of two fp16 numbers: 22 bits, or what
+ * lies above 2^-26 of the query's largest weight times the group's largest scale
+ * among the same 32 tokens.  So do fp32 queries, with 22 bits or what lies above
+ * 2^-34 of their row's largest.  (8-bit codes of fp16 calls are small subnormal
+ * numbers there: where few tokens count, sums of them lose some 2^-21 of their
+ * terms' magnitudes.)  A group whose pair is not finite among the keys that a query
+ * attends to makes its head's output NaN, among the values the elements of that
+ * group.  What lies in the cache beyond a query's length does not reach its output.
  * Consecutive queries of one row share what they read of the cache.
  * Scratch: seedlm_qcache_attend_scratch_bytes, on the stream.
  * Results are the same for the same arguments; the split, and with it the

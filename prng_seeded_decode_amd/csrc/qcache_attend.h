@@ -28,10 +28,13 @@
 // tile earlier still and before those loads (a wait for a load is one for all before it).
 // Pairs pass through LDS, where 4 tokens' are one read.
 //
-// Precision.  p s enters the second product as the sum of two fp16 numbers (22 bits).
-// What subnormal codes cost the sums, and which calls avoid it, is at Row.  fp32 outputs
-// over 8 ragged requests err by 5.8e-7 of their norm, 32-bit sums of dequantised values
-// by 5.9e-7.
+// Precision.  p s enters the second product as the sum of two fp16 numbers, 22 bits down to a
+// smallest step, so what p s is relative to follows the scales of the values (`shift`).  Tiles
+// in which that does not do - one scale above it, or the largest weights on scales far
+// below the others, of all groups or of one - go through a general form of the loop's body, in
+// which each column and group has its own.  What subnormal codes cost the sums, and which
+// calls avoid it, is at Row.  fp32 outputs over 8 ragged requests err by 5.8e-7 of their norm,
+// 32-bit sums of dequantised values by 5.9e-7.
 //
 // Measured (medians, three inputs in turn; one MI355X).  One request of 131071 tokens, 64/8
 // heads of 128, 4 bits, 142 MB: 32.3 us and 5.2 of the join, 4.4 TB/s, where a streaming
@@ -127,6 +130,20 @@ __device__ inline uint32_t pack_rtz(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
 
+// Magnitudes of fp16 scales as numbers: of what follows the finite ones, and from one exponent
+// to the next.  Scales of the least exponent are below 2^-14.
+constexpr uint32_t kScaleInf = 0x7C00u, kScaleExponent = 0x400u;
+constexpr float kLeastShift = -14.f - 15.f;
+// Weights times scales are held to 2^-24 below 2^15 times the power of 2 above all scales.  Scales
+// from 2^-8 of that on are normal, which leaves 2^-31 of the largest weight; a tile whose largest
+// weight is at most 2^4 times one of a token with normal scales has products of 2^2 and more.  The
+// magnitudes of smaller scales, less 1, lie below far_below().  (Where all are of the least
+// exponent, 2^-24 on from 2^-14, none is.)
+constexpr float kFarBelow = 8.f, kNear = 4.f;
+__device__ inline uint32_t far_below(uint32_t exponent) {
+  return exponent == 0 ? 0 : (exponent < 8 ? 1u << (exponent + 2) : kScaleExponent * (exponent - 7)) - 1;
+}
+
 // The largest x of lanes l, l ^ 16, l ^ 32 and l ^ 48.
 __device__ inline float max_of_column(float x) {
   auto largest = [](auto swapped) {
@@ -138,9 +155,31 @@ __device__ inline float max_of_column(float x) {
   return largest(__builtin_amdgcn_permlane32_swap(u, u, false, false));
 }
 
+// The largest x of lanes 32..63.
+__device__ inline uint32_t largest_of_half(uint32_t x) {
+#define SEEDLM_MAX_DPP(ctrl, rows) \
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl, rows, 0xF, false))
+  SEEDLM_MAX_DPP(0x111, 0xF);  // the lane 1, 2, 4 and 8 before in the same 16
+  SEEDLM_MAX_DPP(0x112, 0xF);
+  SEEDLM_MAX_DPP(0x114, 0xF);
+  SEEDLM_MAX_DPP(0x118, 0xF);
+#undef SEEDLM_MAX_DPP
+  return max((uint32_t)__builtin_amdgcn_readlane((int)x, 47), (uint32_t)__builtin_amdgcn_readlane((int)x, 63));
+}
+
 // Keeps what a rare branch does in the branch: the compiler would rather do it always
 // and select.
 __device__ inline void rare() { asm volatile(""); }
+
+// A number that all lanes of a wave hold alike, which the compiler cannot know.
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// A number that the compiler forms where it is used, with all that follows from it, and does not
+// keep in registers through a loop.
+__device__ inline int own(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 template <typename T>
 __device__ void store4(T* p, floatx4 v) {
@@ -272,7 +311,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
   extern __shared__ int32_t s_ends[];  // inclusive sums of the items' units, then the entries
   const seedlm_qcache_attend_args& a = p.a;
   const seedlm_qcache_t& c = a.cache;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int hk = blockIdx.x / p.qtiles, qt = blockIdx.x % p.qtiles;
   const int heads = min(16, p.group - qt * 16);  // of a query in this tile
@@ -300,7 +339,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       sum_units<kThreads>(a.queries, s_ends, [&](int b) {
         return s_entry[b] < 0 ? 0 : units_of(item_of(s_entry + b, a.queries - b).y);
       });
-      units = s_ends[a.queries - 1];
+      units = uniform(s_ends[a.queries - 1]);
     }
     const Runs<kGens> runs(p.slots, units);  // none is empty
     if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -345,6 +384,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       unit += item.x;
     }
 
+    first_query = uniform(first_query);
+    item = make_int2(uniform(item.x), uniform(item.y));
+    begin = uniform(begin), end = uniform(end), unit = uniform(unit);
     const uint8_t* kbase = static_cast<const uint8_t*>(c.k) + hk * c.head_stride + g * (R::kBytes / 4);
     const uint8_t* vbase = static_cast<const uint8_t*>(c.v) + hk * c.head_stride + m * R::kUnitBytes;
     // lanes 0..31 fetch the keys' pairs of the tile's tokens, lanes 32..63 the values'
@@ -355,15 +397,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     // Tile i of this wave: tokens first + 128 i + (0..31); lane l looks after token l % 32.
     const int first = begin + wave * kTile;
     const int tiles = first < end ? (end - first + kUnit - 1) / kUnit : 0;
-    int page = -1, nth = 0;  // of this lane's token in the tile after the next
+    int page = -1, nth = -1;  // of this lane's token in the tile after the next
     auto look_up = [&](int i) {
-      const int tok = first + i * kUnit + (lane & 31);
-      page = -1;
-      if (tok < end) {
-        const uint32_t nr = p.page_size.of(tok);
-        nth = tok - (int)nr * c.page_size;
-        page = table[nr];
-      }
+      const int tok = first + i * kUnit + (lane & 31), at = min(tok, end - 1);
+      const uint32_t nr = p.page_size.of(at);
+      nth = tok < end ? at - (int)nr * c.page_size : -1;
+      page = table[nr];
     };
     struct Tile {
       uint32_t k[2][KD], v[8][VD], pair[NG];
@@ -371,10 +410,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     };
     // Requests the tile that was looked up, and looks up tile `next`.
     auto request = [&](Tile& t, int next) {
-      const bool ok = (uint32_t)page < (uint32_t)c.pages;
+      const bool ok = nth >= 0 && (uint32_t)page < (uint32_t)c.pages;
       const uint32_t off = (uint32_t)page * p.page_unit + (uint32_t)nth * p.token_unit;
-      const uint32_t row = ok ? (uint32_t)page * p.page_pair + (uint32_t)nth * p.token_pair : 0;
-      if (lane < kTile) s_off[wave][lane] = ok ? off : kNoToken;
+      uint32_t row = (uint32_t)page * p.page_pair + (uint32_t)nth * p.token_pair;
+      row = ok ? row : 0;
+      s_off[wave][lane & 31] = ok ? off : kNoToken;  // twice the same
       look_up(next);
       t.live = (uint32_t)__ballot(ok);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -402,6 +442,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     };
 
     Tile even, odd;
+    int i = 0;
     if (tiles > 0) {
       look_up(0);
       request(even, 1);
@@ -478,16 +519,15 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       }
     }
 
-    float base = -INFINITY;  // running maximum (log2) with E added
     float sum = 0.f, osum[NG];  // this lane's share of the weights, and of them times offsets
     floatx4 acc[kAccs];
-    // exponent bits of the largest scale so far, and E with 2^E above it
-    uint32_t largest = 0;
-    auto exponent = [](uint32_t bits) {
-      const float e = (float)(int)(bits >> 10) - 14.f;
-      return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(e)));
-    };
-    float E = exponent(0);
+    // A weight is 2 to the power of score - base, with base the running maximum rounded up to a
+    // whole number, so that it changes by powers of 2, and `shift`: E - 15, with 2^E above the
+    // finite scales of the values of a tile.
+    float base = -INFINITY, shift = kLeastShift;
+    // Magnitudes of scales, as numbers: those from the first on raise the shift, those of which 1
+    // less is below the second are far below 2^E.
+    uint32_t raises = 0, falls = 0;
 #pragma unroll
     for (int j = 0; j < NG; ++j) osum[j] = 0.f;
 #pragma unroll
@@ -497,15 +537,19 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     // mixed-precision instruction in the place of a conversion and a product.
     float zero;
     asm("s_mov_b32 %0, 0" : "=s"(zero));
-    auto compute = [&](const Tile& t, int i) {
+    // Adds tile i.  A tile that only the general form (`any`) can add ends the other's loop, which
+    // adds nothing of it: `bound`.  Where both can, their results are the same bits.
+    int bound = tiles;
+    bool again = false;  // whether the general form was needed
+    auto compute = [&](const Tile& t, int i, auto any) {
       // Pairs: none of a token that does not exist, NaN for what is not finite.
-      uint32_t e = 0;
+      uint32_t e = 0, low = ~0u;  // the token's largest scale, and its least but 0, less 1
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         uint32_t so = (t.live >> (lane & 31)) & 1 ? t.pair[n] : 0;
-        const uint32_t es = so & 0x7C00u, eo = so & 0x7C000000u;
-        if (es == 0x7C00u || eo == 0x7C000000u) so = 0x7E007E00u;
-        else e = max(e, es);
+        const uint32_t es = so & 0x7FFFu, eo = so & 0x7C000000u;
+        if (es >= kScaleInf || eo == 0x7C000000u) so = 0x7E007E00u;
+        else e = max(e, es), low = min(low, es - 1);
         s_pair[wave][n][lane] = so;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -559,29 +603,111 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
       for (int j = 0; j < 8; ++j) most = fmaxf(most, x[j]);
       most = max_of_column(most) * sc;
-      const bool grows = __any(lane >= kTile && e > largest);
-      if (grows || __any(most + E > base)) {
+      // (lanes 32..63 hold values' scales)
+      auto raised = [&] { return (uint32_t)(__ballot(e >= raises) >> 32); };
+      auto fallen = [&] { return (uint32_t)(__ballot(low < falls) >> 32); };
+      auto shift_to = [&](uint32_t exponent) {
+        shift = kLeastShift + (float)(int)exponent;
+        raises = kScaleExponent * (exponent + 1);
+        falls = far_below(exponent);
+      };
+      auto times = [&](float f) {
+        sum *= f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) osum[n] *= f;
+#pragma unroll
+        for (int n = 0; n < kAccs; ++n) acc[n] *= f;
+      };
+      // Scales of group n, as numbers; 0 where the column does not attend to the token.
+      auto scales = [&](int n, uint32_t (&s)[8]) {
+        read_pairs(n, kTile, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] &= (uint32_t)((int32_t)(on << (31 - j)) >> 31) & 0x7FFFu;
+      };
+      // The shift follows the tile's scales, with room for 4 times as much.
+      auto follow = [&] {
+        const uint32_t largest = largest_of_half(e);
+        if (raises == 0 || largest >= raises || (largest != 0 && largest - 1 < falls))
+          shift_to(largest / kScaleExponent + (largest < kScaleExponent ? 0 : 2));
+      };
+      // The maximum may pass what base stands for by a power of 2: twice 2^15 is still what the two
+      // fp16 numbers of a product hold.
+      auto rises = [&](float base) { return most + (shift - 1.f) > base; };
+      float ref = base == -INFINITY ? 0.f : base;
+      if ((raised() | fallen() | __ballot(rises(base))) != 0) {
         rare();
-        if (grows) {
-          if (lane < kTile) e = 0;
+        float up;
+        if constexpr (!any) {
+          if (raises == 0) {
+            rare();
+            follow();
+          }
+          up = rises(base) ? ceilf(most) + shift : base;
+          uint64_t other = raised();
+          if (fallen() != 0) {  // do weights of tokens without such scales come near the largest?
+            rare();
+            uint32_t least = ~0u;
 #pragma unroll
-          for (int d = 1; d < 64; d <<= 1) e = max(e, (uint32_t)__shfl_xor((int)e, d));
-          largest = (uint32_t)__builtin_amdgcn_readfirstlane((int)e);
+            for (int n = 0; n < NG; ++n) least = min(least, t.pair[n] & 0x7FFFu);
+            const uint32_t normal = __ballot(least > falls) >> 32;
+            const uint32_t mine = on & ((normal >> (4 * g) & 15) | (normal >> (16 + 4 * g) & 15) << 4);
+            float next = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) next = fmaxf(next, (mine >> j) & 1 ? x[j] : -INFINITY);
+            other |= __ballot(max_of_column(next) * sc + kNear < most);
+          }
+          // (selections: with branches here the loop would copy its sums from register to register)
+          bound = other != 0 ? i : bound;
+          up = other != 0 ? base : up;
+          times(up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up));
+          ref = other != 0 ? INFINITY : (up == -INFINITY ? 0.f : up);
+        } else {
+          const float was = shift;
+          if ((raised() | fallen()) != 0) follow();
+          const float here = base + (shift - was);
+          up = rises(here) ? ceilf(most) + shift : here;
+          times(up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up));
+          ref = up == -INFINITY ? 0.f : up;
         }
-        const float was = E;
-        E = exponent(largest);
-        const float up = fmaxf(base + (E - was), most + E);
-        const float shrink = up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up);
         base = up;
-        sum *= shrink;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) osum[n] *= shrink;
-#pragma unroll
-        for (int n = 0; n < kAccs; ++n) acc[n] *= shrink;
       }
-      const float ref = base == -INFINITY ? 0.f : base - 15.f;
+      [[maybe_unused]] float lift[NG];  // powers of 2 of each group's weights
+      if constexpr (any) {
+        float weight = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], sc, -ref));
+        for (int j = 0; j < 8; ++j) {
+          x[j] = fmaf(x[j], sc, -ref);
+          weight = fmaxf(weight, x[j]);
+        }
+        weight = max_of_column(weight);
+        float most_lift = 1.f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          // Where scales far below the largest leave a group's largest product as far below what
+          // the weight allows, it is lifted to below 2^15, but by no more than exponents of scales
+          // differ by.  (NaN gives NaN with any lift; a scale of 0 counts as 2^-126.)
+          uint32_t s[8], least = ~0u;
+          scales(n, s);
+          float product = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int exponent = (int)(__float_as_uint((float)as_half2(s[j])[0]) >> 23) - 126;
+            product = fmaxf(product, x[j] + exponent);
+            least = min(least, s[j] - 1);
+          }
+          product = max_of_column(product);
+          const float below = max_of_column(least < far_below((uint32_t)(shift - kLeastShift)) ? 1.f : 0.f);
+          const bool needs = below > 0.f && product < weight + shift + (15.f - kFarBelow - 1.f - kNear);
+          lift[n] = needs ? ldexpf(1.f, (int)fminf(fmaxf(15.f - product, 0.f), 40.f)) : 1.f;
+          most_lift = fmaxf(most_lift, lift[n]);
+        }
+        again = __any(most_lift > 1.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], sc, -ref));
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum += x[j];
 #pragma unroll
@@ -597,19 +723,21 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const half2v a0 = as_half2(vp[2 * w]), a1 = as_half2(vp[2 * w + 1]);
-          osum[n] = fmaf((float)a0[1], x[2 * w], osum[n]);
-          osum[n] = fmaf((float)a1[1], x[2 * w + 1], osum[n]);
-          const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf((float)a0[0], x[2 * w], zero),
-                                                    fmaf((float)a1[0], x[2 * w + 1], zero));
+          float x0 = x[2 * w], x1 = x[2 * w + 1];
+          osum[n] = fmaf((float)a0[1], x0, osum[n]);
+          osum[n] = fmaf((float)a1[1], x1, osum[n]);
+          if constexpr (any) x0 *= lift[n], x1 *= lift[n];
+          const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf((float)a0[0], x0, zero), fmaf((float)a1[0], x1, zero));
           ph[w] = __builtin_bit_cast(uint32_t, h);
-          pl[w] = pack_rtz(fmaf((float)a0[0], x[2 * w], -(float)h[0]),
-                           fmaf((float)a1[0], x[2 * w + 1], -(float)h[1]));
+          pl[w] = pack_rtz(fmaf((float)a0[0], x0, -(float)h[0]), fmaf((float)a1[0], x1, -(float)h[1]));
         }
 #pragma unroll
         for (int k = n * kAccs / NG; k < (n + 1) * kAccs / NG; ++k) {
           const half8 v = R::values(t.v, k);
+          if constexpr (any) acc[k] *= lift[n];
           acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(ph), acc[k], 0, 0, 0);
           acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(pl), acc[k], 0, 0, 0);
+          if constexpr (any) acc[k] *= 1.f / lift[n];
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -618,12 +746,29 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 
     // (A request past the last tile reads the masked token of page 0; without it the paths
     // through the loop would have to wait for one another's loads.)
-    for (int i = 0; i < tiles; ++i) {
-      request(odd, i + 2);
-      compute(even, i);
-      if (++i >= tiles) break;
-      request(even, i + 2);
-      compute(odd, i);
+    constexpr std::false_type kFast;
+    constexpr std::true_type kAny;
+    while (i < tiles) {
+      bound = tiles;
+      for (;;) {
+        request(odd, i + 2);
+        compute(even, i, kFast);
+        if (++i >= bound) break;
+        request(even, i + 2);
+        compute(odd, i, kFast);
+        if (++i >= bound) break;
+      }
+      if (bound != tiles) {  // from that tile on in the general form, as long as it is needed
+        rare();
+        i = bound;
+        look_up(i);
+        request(even, i + 1);
+        do {
+          request(odd, i + 2);
+          compute(even, i, kAny);
+          even = odd;
+        } while (++i < tiles && again);
+      }
     }
 
     // Join the four waves.
@@ -642,7 +787,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
             acc[i] * (1.f / R::kCode) + osum[i * NG / kAccs];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < columns * (D / 4); e += kThreads) {
+    for (int e = own(threadIdx.x); e < columns * (D / 4); e += kThreads) {
       const int h = e / (D / 4), d = e % (D / 4) * 4;
       float mx = -INFINITY, total = 0.f;
 #pragma unroll

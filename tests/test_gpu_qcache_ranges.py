@@ -1,0 +1,123 @@
+"""seedlm_qcache_attend over values whose scales differ from token to token and from group to group by
+more than the bits of a softmax weight.  Offsets of values are 0 here, so that nothing hides what
+codes and scales give; bounds are those of qcache_ref.attend and what is said beside each."""
+import numpy as np
+import pytest
+
+from test_gpu_qcache_attend import check, make, run, terms, widen
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(64, 4, 1), (64, 8, 2), (128, 4, 1), (128, 8, 4), (128, 4, 2), (256, 4, 4), (256, 8, 1)]
+
+
+def values_of(x, b, scale, offset=0.0):
+    """Gives request b's values the scales `scale` ([tokens], [tokens][1][groups] or a number)."""
+    import torch
+
+    p, t = np.array(x["where"][b]).T
+    s = np.zeros(tuple(x["cache"][3][p, t].shape[:-1]))
+    s[:] = scale[:, None, None] if np.ndim(scale) == 1 else scale
+    pairs = np.stack([s, np.full_like(s, offset)], -1).astype(np.float16)
+    assert np.isfinite(pairs).all()
+    x["cache"][3][p, t] = torch.from_numpy(pairs).cuda()
+    x["terms"][b] = terms(x, b)
+
+
+def keys_of(x, b, tokens, offset):
+    """Makes every element of the keys of request b's `tokens` (None: all) `offset`, a number or
+    one for each token."""
+    import torch
+
+    p, t = np.array(x["where"][b])[slice(None) if tokens is None else tokens].T
+    pairs = np.zeros(tuple(x["cache"][2][p, t].shape), np.float16)
+    pairs[..., 1] = np.reshape(offset, (-1, 1, 1))
+    x["cache"][2][p, t] = torch.from_numpy(pairs).cuda()
+    x["terms"][b] = terms(x, b)
+
+
+def uneven(n, dim):
+    """Keys that give n tokens scores of -1 to 0 by a query of ones: weights of all their bits."""
+    return -np.random.default_rng(n).uniform(0, 1, n) / dim
+
+
+def ones(x, value=1.0):
+    import torch
+
+    x["q"][:] = value
+    x["dq"] = torch.from_numpy(x["q"]).cuda()
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", FORMS)
+@pytest.mark.parametrize("power", [0, -10, -17, -24])
+def test_a_large_scale_of_no_weight_costs_the_others_nothing(power, dim, bits, groups, f16):
+    # Token 5, of scale 2^12, has at most e^-63 of another's weight, so 2^-54 of its term: the
+    # reference is without it.
+    lens = [700, 130]
+    x = make([dim, bits, 33], lens, 4, 2, dim, 16, f16, bits, groups)
+    for b, n in enumerate(lens):
+        s = np.full(n, 2.0 ** power)
+        s[5] = 2.0 ** 12
+        values_of(x, b, s)
+        keys_of(x, b, None, uneven(n, dim))
+        keys_of(x, b, [5], -64.0 / dim)
+        x["terms"][b] = [np.delete(a, 5, 0) for a in x["terms"][b]]
+    ones(x)
+    for y in (x, widen(x, 1024)):
+        check(y, run(y, scale=1.0), scale=1.0, lens=[n - 1 for n in lens])
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", [f for f in FORMS if f[2] > 1])
+def test_groups_of_scales_far_apart(dim, bits, groups, f16):
+    # Each group's elements are bounded by that group's own magnitudes.  Scores are 0 in the first
+    # request, which leaves the weights' bits alone.
+    lens = [700, 130, 1]
+    for powers in ([12, -20, -24, 3], [-24, 12, 0, -10], [-10, 2, 11, -3], [-20, -24, -15, -17]):
+        x = make([dim, bits, 34], lens, 4, 2, dim, 16, f16, bits, groups)
+        for b, n in enumerate(lens):
+            rng = np.random.default_rng(b)
+            s = 2.0 ** np.array(powers[:groups]) * np.exp2(rng.uniform(0, 0.9, (n, 1, groups)))
+            values_of(x, b, s)
+        keys_of(x, 0, None, 0.0)
+        for y in (x, widen(x, 1024)):
+            check(y, run(y))
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", FORMS)
+def test_elements_that_large_scales_leave_out(dim, bits, groups, f16):
+    # 128 tokens of scale 2^12 whose codes are 0 in the last half of the elements, before, between
+    # and after tokens of scale 2^-17: those elements keep the bits of the small scales.
+    lens = [700]
+    for first in (0, 256, 512):
+        x = make([dim, bits, 35], lens, 4, 2, dim, 16, f16, bits, groups)
+        s = np.full(700, 2.0 ** -17)
+        s[first: first + 128] = 2.0 ** 12
+        p, t = np.array(x["where"][0])[first: first + 128].T
+        rows = x["cache"][1][p, t].unflatten(-1, (16, -1))
+        rows[..., rows.shape[-1] // 2:] = 0
+        x["cache"][1][p, t] = rows.flatten(-2)
+        values_of(x, 0, s)
+        keys_of(x, 0, None, uneven(700, dim))
+        ones(x)
+        for y in (x, widen(x, 1024)):
+            check(y, run(y, scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", [f for f in FORMS if f[2] > 1])
+def test_a_group_that_the_heaviest_token_leaves_out(dim, bits, groups, f16):
+    # Token 7 has e^10 of the others' weights, a scale of 0 in the first group, where the others have
+    # 2^-20, and theirs in the rest.
+    x = make([dim, bits, 36], [700], 4, 2, dim, 16, f16, bits, groups)
+    s = np.ones((700, 1, groups))
+    s[:, :, 0], s[7, :, 0] = 2.0 ** -20, 0.0
+    values_of(x, 0, s)
+    keys = uneven(700, dim)
+    keys[7] = 10.0 / dim
+    keys_of(x, 0, None, keys)
+    ones(x)
+    for y in (x, widen(x, 1024)):
+        check(y, run(y, scale=1.0), scale=1.0)
