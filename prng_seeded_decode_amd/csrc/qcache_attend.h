@@ -167,6 +167,17 @@ __device__ inline uint32_t largest_of_half(uint32_t x) {
   return max((uint32_t)__builtin_amdgcn_readlane((int)x, 47), (uint32_t)__builtin_amdgcn_readlane((int)x, 63));
 }
 
+// The least x of the 16 lanes of a row.
+__device__ inline int least_of_row(int x) {
+#define SEEDLM_MIN_DPP(ctrl) x = min(x, __builtin_amdgcn_update_dpp(x, x, ctrl, 0xF, 0xF, false))
+  SEEDLM_MIN_DPP(0x121);  // rotated by 1, 2, 4 and 8 lanes
+  SEEDLM_MIN_DPP(0x122);
+  SEEDLM_MIN_DPP(0x124);
+  SEEDLM_MIN_DPP(0x128);
+#undef SEEDLM_MIN_DPP
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
 // Keeps what a rare branch does in the branch: the compiler would rather do it always
 // and select.
 __device__ inline void rare() { asm volatile(""); }
@@ -624,15 +635,22 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[j] &= (uint32_t)((int32_t)(on << (31 - j)) >> 31) & 0x7FFFu;
       };
-      // The shift follows the tile's scales, with room for 4 times as much.
+      // The shift follows the scales of the tokens that all columns attend to which attend to any
+      // of the tile (none must know of others'), with room for 4 times as much.
       auto follow = [&] {
-        const uint32_t largest = largest_of_half(e);
+        uint32_t common = ~0u;
+        if (p.shared > 1) {
+          const int left = least_of_row(length > tile_first ? length : INT32_MAX) - tile_first;
+          common = left < kTile ? (1u << (left & 31)) - 1 : ~0u;
+        }
+        const uint32_t largest = largest_of_half((common >> (lane & 31)) & 1 ? e : 0);
         if (raises == 0 || largest >= raises || (largest != 0 && largest - 1 < falls))
           shift_to(largest / kScaleExponent + (largest < kScaleExponent ? 0 : 2));
       };
       // The maximum may pass what base stands for by a power of 2: twice 2^15 is still what the two
       // fp16 numbers of a product hold.
       auto rises = [&](float base) { return most + (shift - 1.f) > base; };
+      [[maybe_unused]] float followed = shift;
       float ref = base == -INFINITY ? 0.f : base;
       if ((raised() | fallen() | __ballot(rises(base))) != 0) {
         rare();
@@ -664,6 +682,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         } else {
           const float was = shift;
           if ((raised() | fallen()) != 0) follow();
+          followed = shift;
+          if (raised() != 0) shift_to(largest_of_half(e) / kScaleExponent);
           const float here = base + (shift - was);
           up = rises(here) ? ceilf(most) + shift : here;
           times(up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up));
@@ -671,12 +691,27 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         }
         base = up;
       }
-      [[maybe_unused]] float lift[NG];  // powers of 2 of each group's weights
+      // Powers of 2 of the weights: from the shift that the column knows of to the common one, and
+      // of each group's products to their own.
+      [[maybe_unused]] float unit = 1.f, lift[NG];
       if constexpr (any) {
+        float mine = followed;
+        if (shift != followed) {
+          uint32_t largest = 0;
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            uint32_t s[8];
+            scales(n, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) largest = max(largest, s[j] < kScaleInf ? s[j] : 0);
+          }
+          mine = fmaxf(mine, kLeastShift + max_of_column((float)(largest / kScaleExponent)));
+        }
+        unit = ldexpf(1.f, (int)(mine - shift));
         float weight = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[j] = fmaf(x[j], sc, -ref);
+          x[j] = fmaf(x[j], sc, (shift - mine) - ref);
           weight = fmaxf(weight, x[j]);
         }
         weight = max_of_column(weight);
@@ -696,8 +731,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
             least = min(least, s[j] - 1);
           }
           product = max_of_column(product);
-          const float below = max_of_column(least < far_below((uint32_t)(shift - kLeastShift)) ? 1.f : 0.f);
-          const bool needs = below > 0.f && product < weight + shift + (15.f - kFarBelow - 1.f - kNear);
+          const float below = max_of_column(least < far_below((uint32_t)(mine - kLeastShift)) ? 1.f : 0.f);
+          const bool needs = below > 0.f && product < weight + mine + (15.f - kFarBelow - 1.f - kNear);
           lift[n] = needs ? ldexpf(1.f, (int)fminf(fmaxf(15.f - product, 0.f), 40.f)) : 1.f;
           most_lift = fmaxf(most_lift, lift[n]);
         }
@@ -709,7 +744,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(fmaf(x[j], sc, -ref));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += x[j];
+      for (int j = 0; j < 8; ++j) sum += any ? x[j] * unit : x[j];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         uint32_t vp[8];
@@ -724,8 +759,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         for (int w = 0; w < 4; ++w) {
           const half2v a0 = as_half2(vp[2 * w]), a1 = as_half2(vp[2 * w + 1]);
           float x0 = x[2 * w], x1 = x[2 * w + 1];
-          osum[n] = fmaf((float)a0[1], x0, osum[n]);
-          osum[n] = fmaf((float)a1[1], x1, osum[n]);
+          osum[n] = fmaf((float)a0[1], any ? x0 * unit : x0, osum[n]);
+          osum[n] = fmaf((float)a1[1], any ? x1 * unit : x1, osum[n]);
           if constexpr (any) x0 *= lift[n], x1 *= lift[n];
           const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf((float)a0[0], x0, zero), fmaf((float)a1[0], x1, zero));
           ph[w] = __builtin_bit_cast(uint32_t, h);
@@ -734,10 +769,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
 #pragma unroll
         for (int k = n * kAccs / NG; k < (n + 1) * kAccs / NG; ++k) {
           const half8 v = R::values(t.v, k);
-          if constexpr (any) acc[k] *= lift[n];
+          if constexpr (any) acc[k] *= lift[n] / unit;
           acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(ph), acc[k], 0, 0, 0);
           acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, as_half8(pl), acc[k], 0, 0, 0);
-          if constexpr (any) acc[k] *= 1.f / lift[n];
+          if constexpr (any) acc[k] *= unit / lift[n];
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -4,7 +4,8 @@ codes and scales give; bounds are those of qcache_ref.attend and what is said be
 import numpy as np
 import pytest
 
-from test_gpu_qcache_attend import check, make, run, terms, widen
+import qcache_ref as Q
+from test_gpu_qcache_attend import check, make, run, run_rows, terms, widen
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,41 @@ def test_a_group_that_the_heaviest_token_leaves_out(dim, bits, groups, f16):
     ones(x)
     for y in (x, widen(x, 1024)):
         check(y, run(y, scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("heads,kv", [(4, 2), (16, 2), (5, 1)])
+@pytest.mark.parametrize("dim,bits,groups", [(128, 4, 2), (64, 8, 1), (256, 4, 4)])
+def test_scales_past_one_querys_length_leave_its_bits(dim, bits, groups, heads, kv, f16):
+    # Queries that share their reading: finite scales that only the longer ones attend to, behind
+    # other tiles and in the first.
+    import torch
+
+    for n, at, lens in ((400, 380, [100, 400, 390, 380, 10, 381]), (30, 5, [5, 30, 6, 1, 4, 5])):
+        x = make([16, heads, n], [n], heads, kv, dim, 16, f16, bits, groups)
+        g = torch.Generator(device="cuda").manual_seed(n)
+        q = torch.randn((6, heads, dim), generator=g, device="cuda").to(x["dq"].dtype)
+        host, rows = q.cpu().numpy(), [0] * 6
+        s = np.full(n, 2.0 ** -12)
+        values_of(x, 0, s)
+        clean = [run_rows(y, q, rows, lens) for y in (x, widen(x, 9000))]
+        s[at:] = 2.0 ** 12
+        values_of(x, 0, s)
+        short = [i for i in range(6) if lens[i] <= at]
+        for y, was in zip((x, widen(x, 9000)), clean):
+            got = run_rows(y, q, rows, lens)
+            for i in short:
+                assert np.array_equal(got[i], was[i]), i
+            check(y, got[short], lens=[lens[i] for i in short], rows=[0] * len(short), q=host[short])
+            for i in set(range(6)) - set(short):
+                ref, tol = Q.attend(host[i].astype(np.float64), *(a[: lens[i]] for a in y["terms"][0]),
+                                    np.float64(np.float32(dim ** -0.5)), f16)
+                # 32 tokens of which some have these scales: weights times scales, 2^15 standing for
+                # the largest weight times 2^15 or less, are cut to 2^-24, so to 2^-24 of it, and the
+                # products' sum to that many times the codes.
+                tol += 2.0 ** -24 * np.repeat((x["terms"][0][3] / s[:, None, None])[at // 32 * 32:][:32].sum(0),
+                                              heads // kv, 0)
+                err = np.abs(got[i] - ref)
+                if f16:
+                    err[(np.abs(ref) + tol >= 65520) & (got[i] == np.copysign(np.inf, ref))] = 0
+                assert np.all(err <= tol), (i, float((err - tol).max()))
