@@ -144,6 +144,15 @@ __device__ inline uint32_t far_below(uint32_t exponent) {
   return exponent == 0 ? 0 : (exponent < 8 ? 1u << (exponent + 2) : kScaleExponent * (exponent - 7)) - 1;
 }
 
+// Scores of this and more (in powers of 2) are held in fp32 to steps of a half or more, which a
+// shift is lost in.  Their maximum is the largest of the rounded products, so it is taken from
+// those.
+constexpr float kFar = 0x1p22f;
+__device__ inline float minus(float x, float scale, float from) {
+#pragma clang fp contract(off)
+  return x * scale - from;
+}
+
 // The largest x of lanes l, l ^ 16, l ^ 32 and l ^ 48.
 __device__ inline float max_of_column(float x) {
   auto largest = [](auto swapped) {
@@ -539,6 +548,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     // Magnitudes of scales, as numbers: those from the first on raise the shift, those of which 1
     // less is below the second are far below 2^E.
     uint32_t raises = 0, falls = 0;
+    // Columns whose maximum and shift have no sum in fp32: base is the maximum, weights are of
+    // (score - base) - shift.
+    uint64_t far = 0;
+    auto is_far = [&] { return (far >> lane & 1) != 0; };
 #pragma unroll
     for (int j = 0; j < NG; ++j) osum[j] = 0.f;
 #pragma unroll
@@ -649,10 +662,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       };
       // The maximum may pass what base stands for by a power of 2: twice 2^15 is still what the two
       // fp16 numbers of a product hold.
-      auto rises = [&](float base) { return most + (shift - 1.f) > base; };
+      auto rises = [&](float base) { return any && is_far() ? most > base : most + (shift - 1.f) > base; };
       [[maybe_unused]] float followed = shift;
       float ref = base == -INFINITY ? 0.f : base;
-      if ((raised() | fallen() | __ballot(rises(base))) != 0) {
+      if ((raised() | fallen() | far | __ballot(rises(base))) != 0) {
         rare();
         float up;
         if constexpr (!any) {
@@ -661,7 +674,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
             follow();
           }
           up = rises(base) ? ceilf(most) + shift : base;
-          uint64_t other = raised();
+          uint64_t other = raised() | far | __ballot(fabsf(up) >= kFar && up != -INFINITY);
           if (fallen() != 0) {  // do weights of tokens without such scales come near the largest?
             rare();
             uint32_t least = ~0u;
@@ -684,9 +697,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
           if ((raised() | fallen()) != 0) follow();
           followed = shift;
           if (raised() != 0) shift_to(largest_of_half(e) / kScaleExponent);
-          const float here = base + (shift - was);
-          up = rises(here) ? ceilf(most) + shift : here;
-          times(up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(base - up));
+          const float here = is_far() ? base : base + (shift - was);
+          up = rises(here) ? ceilf(most) + (is_far() ? 0.f : shift) : here;
+          const float top = is_far() ? up : up - shift, had = is_far() ? was : 0.f;
+          far = __ballot(fabsf(top) >= kFar && top != -INFINITY);
+          up = is_far() ? top : top + shift;
+          times(up == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((base - up) + (had - (is_far() ? shift : 0.f))));
           ref = up == -INFINITY ? 0.f : up;
         }
         base = up;
@@ -711,7 +727,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
         float weight = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[j] = fmaf(x[j], sc, (shift - mine) - ref);
+          const float y = fmaf(x[j], sc, (shift - mine) - ref);
+          x[j] = is_far() ? minus(x[j], sc, ref) - mine : y;
           weight = fmaxf(weight, x[j]);
         }
         weight = max_of_column(weight);
@@ -736,7 +753,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
           lift[n] = needs ? ldexpf(1.f, (int)fminf(fmaxf(15.f - product, 0.f), 40.f)) : 1.f;
           most_lift = fmaxf(most_lift, lift[n]);
         }
-        again = __any(most_lift > 1.f);
+        again = (far | __ballot(most_lift > 1.f)) != 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j]);
       } else {
@@ -813,6 +830,15 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     for (int n = 0; n < NG; ++n) {
       osum[n] += __shfl_xor(osum[n], 16);
       osum[n] += __shfl_xor(osum[n], 32);
+    }
+    if (far != 0) {  // sums of weights with the shift in their base
+      rare();
+      const float unit = is_far() ? ldexpf(1.f, (int)shift) : 1.f;
+      sum *= unit;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) osum[n] *= unit;
+#pragma unroll
+      for (int n = 0; n < kAccs; ++n) acc[n] *= unit;
     }
     if (g == 0) s_ml[wave][m] = make_float2(base, sum);
     if (m < columns) {

@@ -1,6 +1,7 @@
-"""seedlm_qcache_attend over values whose scales differ from token to token and from group to group by
-more than the bits of a softmax weight.  Offsets of values are 0 here, so that nothing hides what
-codes and scales give; bounds are those of qcache_ref.attend and what is said beside each."""
+"""seedlm_qcache_attend where numbers lie far apart: scores whose steps in fp32 are whole powers of
+two, and values' scales that differ from token to token and from group to group by more than the
+bits of a softmax weight.  Offsets of values are 0 here, so that nothing hides what codes and
+scales give; bounds are those of qcache_ref.attend and what is said beside each."""
 import numpy as np
 import pytest
 
@@ -47,6 +48,42 @@ def ones(x, value=1.0):
 
     x["q"][:] = value
     x["dq"] = torch.from_numpy(x["q"]).cuda()
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", FORMS)
+@pytest.mark.parametrize("key,query", [(2000.0, 2000.0), (60000.0, 60000.0), (-500.0, 3000.0)])
+def test_scores_past_24_bits(key, query, dim, bits, groups, f16):
+    # All scores of a request are one number, of 2^26 to 2^40 in powers of 2, where fp32's steps are
+    # 4 to 2^17: weights of one another's size all the same, whole and split.  The mean of the
+    # values, exact in the scores, so that the bound is that of scores of 0.
+    lens = [700, 40, 1, 129]
+    x = make([dim, bits, 31], lens, 4, 2, dim, 16, f16, bits, groups)
+    for b in range(4):
+        values_of(x, b, 0.25 if bits == 4 else 0.02)
+        keys_of(x, b, None, 0.0)
+    ones(x, query)
+    want = [[a.copy() for a in t] for t in x["terms"]]
+    for b in range(4):
+        keys_of(x, b, None, key)
+    x["terms"] = want
+    for y in (x, widen(x, 1024)):
+        check(y, run(y, scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("f16", [True, False])
+def test_the_largest_of_scores_past_24_bits_takes_all(f16):
+    # One token above the others by far more than a step, in each of three tiles and waves.
+    for at in (3, 70, 699):
+        x = make([at, 32], [700], 4, 2, 128, 16, f16, 4, 1)
+        values_of(x, 0, 0.5)
+        keys_of(x, 0, None, 1900.0)
+        keys_of(x, 0, [at], 2000.0)
+        ones(x, 2000.0)
+        _, _, v, _ = x["terms"][0]
+        for y in (x, widen(x, 1024)):
+            got = run(y, scale=1.0)
+            assert np.array_equal(got[0], np.repeat(v[at], 2, 0))  # multiples of 1/2 below 8
 
 
 @pytest.mark.parametrize("f16", [True, False])
