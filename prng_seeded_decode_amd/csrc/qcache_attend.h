@@ -76,7 +76,8 @@ struct Args {
   int group;    // query heads per cache head
   int qtiles;   // ceil(group / 16)
   int shared;   // queries of an item at most
-  int slots;    // runs of units; 0: one workgroup per `shared` queries
+  int slots;    // runs of units; 0: a workgroup per query, those that go on with another's item idle
+  int rows;     // of the grid
   int cap;      // largest length: min(max_len, max_pages * page_size)
   uint32_t page_unit, token_unit;  // strides of codes in units of 16 bytes
   uint32_t page_pair, token_pair;  // strides of pairs in rows of pairs
@@ -337,17 +338,19 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
   const int heads = min(16, p.group - qt * 16);  // of a query in this tile
   const int head0 = hk * p.group + qt * 16;
 
-  // The inclusive sums of the items' units, then the entries.  Up to 64 queries that share
-  // nothing are a lane each: every wave forms and writes the sums itself (all write the
-  // same numbers, so none waits for another).
-  const bool few = p.shared == 1 && a.queries <= 64;
+  // The inclusive sums of the items' units, then the entries.  Up to 64 queries of which none goes
+  // on with another's item are a lane each: every wave forms and writes the sums itself (all write
+  // the same numbers, so none waits for another).
+  bool few = p.slots > 0 && a.queries <= 64;
   int unit = 0, unit_end = 1, run_begin = 0;
+  int block_query = blockIdx.y, block_row = 0;  // of a call without a split
   int32_t* s_entry = s_ends;
   if (p.slots > 0) {
     s_entry = s_ends + a.queries;
     int units;
+    const int len = few && lane < a.queries ? item_entry(p, lane) : 0;
+    few = few && !__any(len < 0);
     if (few) {
-      const int len = lane < a.queries ? length_of(p, lane) : 0;
       const int upto = wave_sums(units_of(len));
       if (lane < a.queries) s_ends[lane] = upto, s_entry[lane] = len;
       units = __builtin_amdgcn_readlane(upto, 63);
@@ -372,15 +375,33 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     if ((int)blockIdx.y >= runs.slots) return;
     run_begin = unit = runs.begin(blockIdx.y);
     unit_end = runs.begin(blockIdx.y + 1);
-  } else if (p.shared > 1) {  // `shared` queries, which are an item or several
-    unit_end = min(p.shared, a.queries - (int)blockIdx.y * p.shared);
-    if ((int)threadIdx.x < unit_end)
-      s_entry[threadIdx.x] = item_entry(p, blockIdx.y * p.shared + threadIdx.x);
-    __syncthreads();
+  } else if (p.shared > 1) {
+    // First the queries that certainly start an item, then the others, so that those which only
+    // find that they do not end while the items go on.  Every wave writes the entries of the
+    // query and of those that may go on with it.  A workgroup for `shared` queries would take
+    // their items one after another: 16 requests of a token each, 32 cache heads, 500 tokens, 88
+    // against 10.9 us; where all are pieces the idle workgroups cost up to 1.2 of 49 us.
+    int nth = 0;  // of the `shared` queries that may be one item
+    const int starts = (a.queries + p.shared - 1) / p.shared;
+    if (block_query < starts) {
+      block_query *= p.shared;
+    } else {
+      const int other = block_query - starts, of = other / (p.shared - 1);
+      nth = 1 + other - of * (p.shared - 1);
+      block_query = of * p.shared + nth;
+    }
+    const int n = min(p.shared - nth, a.queries - block_query);
+    const int entry = lane < n ? item_entry(p, block_query + lane) : 0;
+    block_row = a.rows[block_query];
+    if (uniform(entry) < 0) return;
+    if (lane < n) s_entry[lane] = entry;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    unit_end = n;
   }
   while (unit < unit_end) {
     // The next item of the run and the tokens of it that lie in the run.
-    int first_query = blockIdx.y, begin = 0, end;
+    int first_query, begin = 0, end;
     bool whole = true;
     const bool starts_run = unit == run_begin;
     int2 item;
@@ -397,11 +418,10 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       unit = upto;
       if (begin >= end) continue;  // the run ends before the item's tokens do begin
     } else {
-      first_query = blockIdx.y * p.shared + unit;
-      item = p.shared > 1 ? item_of(s_entry + unit, unit_end - unit)
-                          : make_int2(1, length_of(p, first_query));
+      first_query = block_query;
+      item = p.shared > 1 ? item_of(s_entry, unit_end) : make_int2(1, length_of(p, first_query));
       end = item.y;
-      unit += item.x;
+      unit = unit_end;
     }
 
     first_query = uniform(first_query);
@@ -412,7 +432,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     // lanes 0..31 fetch the keys' pairs of the tile's tokens, lanes 32..63 the values'
     const uint32_t* pairs = static_cast<const uint32_t*>(lane < kTile ? c.k_scale : c.v_scale) +
                             hk * c.scale_head_stride;
-    const int32_t* table = a.table + (a.rows ? (int64_t)a.rows[first_query] : first_query) * a.table_stride;
+    int row = first_query;
+    if (a.rows) row = p.slots == 0 && p.shared > 1 ? block_row : a.rows[first_query];
+    const int32_t* table = a.table + (int64_t)row * a.table_stride;
 
     // Tile i of this wave: tokens first + 128 i + (0..31); lane l looks after token l % 32.
     const int first = begin + wave * kTile;
@@ -475,7 +497,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     const int query = first_query + nth_query, head = head0 + column - nth_query * heads;
     int length = item.y;
     if (p.shared > 1) {
-      length = s_entry[p.slots > 0 ? query : query - blockIdx.y * p.shared];
+      length = s_entry[p.slots > 0 ? query : query - block_query];
       length = length < 0 ? -1 - length : length;
     }
 
@@ -961,8 +983,8 @@ int run_groups(const Args& p, hipStream_t s) {
   const bool split = p.slots > 0;
   const auto kernel = streams(a, p.cap) ? qcache_attend_kernel<D, BITS, NG, WIDE, may_stream(D * BITS)>
                                         : qcache_attend_kernel<D, BITS, NG, WIDE, false>;
-  const int rows = split ? p.slots : (a.queries + p.shared - 1) / p.shared;
-  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, rows), dim3(kThreads), (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
+  hipLaunchKernelGGL(kernel, dim3(a.cache.kv_heads * p.qtiles, p.rows), dim3(kThreads),
+                     (split ? 2 * a.queries : p.shared) * sizeof(int32_t), s, p);
   if (split && (int64_t)a.heads * a.queries >= kManyJoins)
     hipLaunchKernelGGL((qcache_attend_join_kernel<D, WIDE, 64>), dim3((a.heads + 3) / 4, a.queries),
                        dim3(kThreads), 0, s, p);

@@ -22,6 +22,13 @@ int shared_of(const seedlm_qcache_attend_args& a) {
   return a.rows && group_of(a) < 16 ? 16 / group_of(a) : 1;
 }
 
+// Queries of a row of the table, as far as the call's sizes say (which query has which row
+// lies in device memory), and of an item.
+int per_row(const seedlm_qcache_attend_args& a) {
+  return a.rows ? std::max(1, a.queries / a.table_rows) : 1;
+}
+int in_item(const seedlm_qcache_attend_args& a) { return std::min(shared_of(a), per_row(a)); }
+
 // Whether items are the workgroups: then an item's steps of kUnit tokens follow one
 // another, but the sums, the partials and the second launch (4 to 5 us) fall away.  That
 // pays up to so many steps, and up to twice as many where items fill half the chip.  Time
@@ -34,15 +41,19 @@ int shared_of(const seedlm_qcache_attend_args& a) {
 // every compute unit runs of even length gain nothing until lengths differ much: 64
 // requests 31.6 and 38.9 at 2048.  Items of several queries are as long as their
 // neighbours: 128 queries of one request of 2048 tokens (256 workgroups) 21.5 and 25.6,
-// 512 of 2048 46.6 and 56.5, 512 of 8192 159 and 164.
+// 512 of 2048 46.6 and 56.5, 512 of 8192 159 and 164.  That holds from twice as many queries
+// of a row as an item takes (4 of 128 in a table of 64 rows 42.0 and 49.0); with fewer the
+// items may be single tokens of requests that have nothing in common (64 rows of 8 queries,
+// ragged up to 8000, 136 and 120, but 128 of 4000 124 and 129).
 bool unsplit(const seedlm_qcache_attend_args& a) {
-  const int64_t items = (a.queries + shared_of(a) - 1) / shared_of(a);
+  const int64_t items = (a.queries + in_item(a) - 1) / in_item(a);
   const int64_t workgroups = items * a.cache.kv_heads * qtiles_of(a);
   int steps = a.cache.head_dim == 64 ? 7 : (a.cache.head_dim == 128 ? 6 : 4);
   const int cus = device_cu_count();
   if (2 * workgroups >= cus) steps *= 2;
   if (workgroups >= 2 * cus) steps = std::max(steps, 16 * 128 / a.cache.head_dim);
-  if (shared_of(a) > 1 && workgroups >= cus) steps = workgroups >= 4 * cus ? 64 : 32;
+  if (per_row(a) >= 2 * shared_of(a) && shared_of(a) > 1 && workgroups >= cus)
+    steps = workgroups >= 4 * cus ? 64 : 32;
   return cap_of(a) <= steps * kUnit;
 }
 
@@ -85,6 +96,7 @@ int launch_qcache_attend(const seedlm_qcache_attend_args& a, void* scratch, hipS
   p.qtiles = qtiles_of(a);
   p.shared = shared_of(a);
   p.slots = slots_of(a);
+  p.rows = p.slots > 0 ? p.slots : a.queries;
   p.cap = cap_of(a);
   p.page_unit = (uint32_t)(c.page_stride / 16);
   p.token_unit = (uint32_t)(c.token_stride / 16);
