@@ -128,6 +128,13 @@ def _cache(k_cache, v_cache):
     return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), pages, *strides[0], size, heads, dim)
 
 
+def _qcache_of(k_cache, v_cache, k_scale, v_scale, x):
+    """The cache of a call whose rows x are [tokens][heads][head_dim]."""
+    if x.dim() != 3:
+        raise ValueError("q and the outputs must be [tokens][heads][head_dim]")
+    return _qcache(k_cache, v_cache, k_scale, v_scale, x.shape[2])
+
+
 def _qcache(k_cache, v_cache, k_scale, v_scale, dim):
     import torch
 
@@ -152,7 +159,7 @@ def _qcache(k_cache, v_cache, k_scale, v_scale, dim):
         raise ValueError("the strides of the scales must be whole pairs")
     pages, size, heads, width = k_cache.shape
     groups = k_scale.shape[3]
-    if groups == 0 or dim % groups or width * 8 % dim:
+    if groups == 0 or dim == 0 or dim % groups or width * 8 % dim:
         raise ValueError("rows and scales do not fit head_dim")
     return _QCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                    pages, *at[0], *(s // 2 for s in at[2]), size, heads, dim, width * 8 // dim,
@@ -326,7 +333,7 @@ class QCacheAppendCall(_Call):
                  v_scale, interleaved=False, stream=None):
         keep = (q, k, v, cos, sin, positions, slots, q_out, k_cache, v_cache, k_scale, v_scale)
         device = _on_device(keep)
-        cache = _qcache(k_cache, v_cache, k_scale, v_scale, q.shape[-1])
+        cache = _qcache_of(k_cache, v_cache, k_scale, v_scale, q)
         args = _append_args(_QAppendArgs, cache, q, k, v, cos, sin, positions, slots, q_out,
                             interleaved)
         self._set("seedlm_qcache_append", lib().seedlm_qcache_append, (ctypes.byref(args),), keep,
@@ -346,7 +353,7 @@ class QCacheReadCall(_Call):
             raise ValueError("k_out or v_out must be given")
         keep = (k_cache, v_cache, k_scale, v_scale, slots, *outs)
         device = _on_device(keep)
-        cache = _qcache(k_cache, v_cache, k_scale, v_scale, outs[0].shape[-1])
+        cache = _qcache_of(k_cache, v_cache, k_scale, v_scale, outs[0])
         code, tokens = _dtype_code(outs[0]), slots.numel()
         strides = [0 if t is None else _heads(what, t, tokens, cache.kv_heads, cache.head_dim,
                                               outs[0].dtype)
@@ -369,7 +376,7 @@ class QCacheAttendCall(_Call):
         keep = (q, k_cache, v_cache, k_scale, v_scale, table, lens, out) + (
             () if rows is None else (rows,))
         device = _on_device(keep)
-        cache = _qcache(k_cache, v_cache, k_scale, v_scale, q.shape[-1])
+        cache = _qcache_of(k_cache, v_cache, k_scale, v_scale, q)
         args = _attend_args(_QAttendArgs, cache, q, table, lens, out, scale, max_len, rows)
         self._set("seedlm_qcache_attend", lib().seedlm_qcache_attend, (ctypes.byref(args),), keep,
                   device, stream)
