@@ -589,13 +589,12 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
     bool again = false;  // whether the general form was needed
     auto compute = [&](const Tile& t, int i, auto any) {
       // Pairs: none of a token that does not exist, NaN for what is not finite.
-      uint32_t e = 0, low = ~0u;  // the token's largest scale, and its least but 0, less 1
+      uint32_t e = 0, low = ~0u;  // the token's largest scale (or NaN), and its least but 0, less 1
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         uint32_t so = (t.live >> (lane & 31)) & 1 ? t.pair[n] : 0;
-        const uint32_t es = so & 0x7FFFu, eo = so & 0x7C000000u;
-        if (es >= kScaleInf || eo == 0x7C000000u) so = 0x7E007E00u;
-        else e = max(e, es), low = min(low, es - 1);
+        if ((so & 0x7FFFu) >= kScaleInf || (so & 0x7C000000u) == 0x7C000000u) so = 0x7E007E00u;
+        e = max(e, so & 0x7FFFu), low = min(low, (so & 0x7FFFu) - 1);
         s_pair[wave][n][lane] = so;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -689,6 +688,15 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
       float ref = base == -INFINITY ? 0.f : base;
       if ((raised() | fallen() | far | __ballot(rises(base))) != 0) {
         rare();
+        if (__any(e >= kScaleInf)) {  // the largest of the finite ones
+          rare();
+          e = 0;
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const uint32_t so = (t.live >> (lane & 31)) & 1 ? t.pair[n] : 0;
+            if ((so & 0x7FFFu) < kScaleInf && (so & 0x7C000000u) != 0x7C000000u) e = max(e, so & 0x7FFFu);
+          }
+        }
         float up;
         if constexpr (!any) {
           if (raises == 0) {
@@ -961,7 +969,10 @@ __global__ __launch_bounds__(kThreads) void qcache_attend_join_kernel(const Args
 // and 23.5 at 68 MB; the lengths are not known here, and ragged ones of half the bound lose
 // 2 to 4%.  64 dimensions of 8 bits gain as much (58.3 and 64.2 at 300), rows of
 // 32 bytes nothing (81.8 and 80.6), and rows of 256 bytes lose (39 and 34, 73 and 65, 187
-// and 169).
+// and 169).  Calls with `rows` stay in the caches, since queries of one row that lie in
+// different items read its pages again: 256 pieces of 8 queries 243 and 225, 16 of 16 68 and
+// 62.  Where each row has one token, that costs them the gain (128 requests of 32 cache
+// heads and 64 dimensions at 2000 tokens 184 and 197).
 constexpr bool may_stream(int row_bits) { return row_bits == 512 || row_bits == 1024; }
 
 inline bool streams(const seedlm_qcache_attend_args& a, int cap) {
