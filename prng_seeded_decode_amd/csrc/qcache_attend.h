@@ -33,8 +33,8 @@
 // in which that does not do - one scale above it, or the largest weights on scales far
 // below the others, of all groups or of one - go through a general form of the loop's body, in
 // which each column and group has its own.  What subnormal codes cost the sums, and which
-// calls avoid it, is at Row.  fp32 outputs over 8 ragged requests err by 5.8e-7 of their norm,
-// 32-bit sums of dequantised values by 5.9e-7.
+// calls avoid it, is at Row.  fp32 outputs over 8 ragged requests err by 5.2 to 5.7e-7 of their
+// norm, 32-bit sums of dequantised values by 5.4 to 6.0e-7.
 //
 // Measured (medians, three inputs in turn; one MI355X).  One request of 131071 tokens, 64/8
 // heads of 128, 4 bits, 142 MB: 32.3 us and 5.2 of the join, 4.4 TB/s, where a streaming
@@ -127,8 +127,8 @@ __device__ int4 join_of(const Runs<GENS>& runs, int first, int u0, int u1) {
 __device__ inline half8 as_half8(v4u v) { return __builtin_bit_cast(half8, v); }
 __device__ inline half2v as_half2(uint32_t v) { return __builtin_bit_cast(half2v, v); }
 
-__device__ inline uint32_t pack_rtz(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+__device__ inline uint32_t pack(float a, float b) {  // rounded to nearest
+  return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
 }
 
 // Magnitudes of fp16 scales as numbers: of what follows the finite ones, and from one exponent
@@ -809,9 +809,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(D, BITS, NG, WIDE)) void q
           osum[n] = fmaf((float)a0[1], any ? x0 * unit : x0, osum[n]);
           osum[n] = fmaf((float)a1[1], any ? x1 * unit : x1, osum[n]);
           if constexpr (any) x0 *= lift[n], x1 *= lift[n];
+          // (The first is cut, which keeps it finite, the second rounded: cut too, sums would come
+          // out low by 7.5e-8 on average.)
           const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf((float)a0[0], x0, zero), fmaf((float)a1[0], x1, zero));
           ph[w] = __builtin_bit_cast(uint32_t, h);
-          pl[w] = pack_rtz(fmaf((float)a0[0], x0, -(float)h[0]), fmaf((float)a1[0], x1, -(float)h[1]));
+          pl[w] = pack(fmaf((float)a0[0], x0, -(float)h[0]), fmaf((float)a1[0], x1, -(float)h[1]));
         }
 #pragma unroll
         for (int k = n * kAccs / NG; k < (n + 1) * kAccs / NG; ++k) {

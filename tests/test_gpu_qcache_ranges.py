@@ -197,3 +197,21 @@ def test_scales_past_one_querys_length_leave_its_bits(dim, bits, groups, heads, 
                 if f16:
                     err[(np.abs(ref) + tol >= 65520) & (got[i] == np.copysign(np.inf, ref))] = 0
                 assert np.all(err <= tol), (i, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("dim,bits,groups", FORMS)
+def test_weights_are_not_low_on_average(dim, bits, groups):
+    # Requests of one token with scores of any fraction, fp32: an output is its value times the
+    # ratio of the weight's two parts to the weight.  Each ratio errs by at most 2^-22, half a step
+    # of the second part, and with the roundings of a product, the join and the division by no more
+    # than 2^-21; nearest roundings are as often high as low, so the mean over 512 columns lies
+    # within 2^-21 / sqrt(512) < 2^-25.  (Parts that are cut leave 7.5e-8, more than 2^-24.)
+    x = make([dim, groups, 5], [1] * 64, 8, 2, dim, 16, False, bits, groups)
+    for b in range(64):
+        values_of(x, b, 1.0)
+    got = run(x)
+    value = np.stack([np.repeat(x["terms"][b][2][0], 4, 0) for b in range(64)])
+    with np.errstate(divide="ignore", invalid="ignore"):
+        error = np.where(value > 0, got / value - 1, 0.0).sum(2) / (value > 0).sum(2)
+    assert np.abs(error).max() <= 2.0 ** -21
+    assert abs(error.mean()) < 2.0 ** -25, error.mean()
