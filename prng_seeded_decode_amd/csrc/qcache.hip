@@ -245,9 +245,9 @@ struct AppendArgs {
   bool stream;          // q passes the caches
 };
 
-// VEC: k, v and the angles in aligned fours.  N: pairs of a unit of q, 8 or 1.  Waves side
-// by side: five in 128 dimensions (38.3 us for 4097 tokens of 32 heads with four, 34.5 with
-// five, 46 with six, whose loads no longer fit the registers together).
+// VEC: k, v and the angles in aligned fours.  N: pairs of a unit of q, 8 with VEC, else 1.
+// Waves side by side: five in 128 dimensions (38.3 us for 4097 tokens of 32 heads with four,
+// 34.5 with five, 46 with six, whose loads no longer fit the registers together).
 template <int D, int BITS, int NG, bool VEC, int N, typename T>
 __global__ __launch_bounds__(kThreads, D == 64 ? 8 : (D == 128 ? 5 : 2)) void qcache_append_kernel(const AppendArgs p) {
   const seedlm_qcache_append_args& a = p.a;
@@ -517,6 +517,10 @@ int launch_qcache_append(const seedlm_qcache_append_args& a, hipStream_t s) {
   const int D = a.cache.head_dim;
   const bool vec = fours(a.k, a.k_stride, a.x_dtype) && fours(a.v, a.v_stride, a.x_dtype) &&
                    a.rot % 8 == 0 && aligned16(a.cos) && aligned16(a.sin);
+  // One form for all of a call: what keeps q from units of 8 pairs (rot no multiple of 16, a row
+  // or an angle off 16 bytes) nearly always does the same to k and v, which a projection wrote
+  // beside it.  4097 tokens of 32/32 heads of 128, fp16, 36.7 us and by single elements 109,
+  // 16 tokens of 32/8 4.8 and 11.2, whichever tensor it is that does not fit.
   const bool wide = vec && wide_units(a);
   AppendArgs p{a, RowSplit(a.cache.kv_heads), divisor((uint32_t)a.cache.page_size), wide ? D / 16 : D / 2, {}, false};
   if (a.heads > 1024) p.split.tokens = 1;  // the grid's second dimension is short

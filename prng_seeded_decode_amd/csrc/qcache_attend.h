@@ -36,15 +36,15 @@
 // calls avoid it, is at Row.  fp32 outputs over 8 ragged requests err by 5.2 to 5.7e-7 of their
 // norm, 32-bit sums of dequantised values by 5.4 to 6.0e-7.
 //
-// Measured (medians, three inputs in turn; one MI355X).  One request of 131071 tokens, 64/8
-// heads of 128, 4 bits, 142 MB: 32.3 us and 5.2 of the join, 4.4 TB/s, where a streaming
-// read has 6.2; 64 ragged ones up to 16384, 32/8 heads: 116 to 128 and 5.2 (the inputs
-// between 97 and 147); 16 ragged ones up to 8192, 64/8 heads, two groups: 23.7 and 4.6.
-// Memory and the vector units bound them together: in 67 to 80% of the SIMDs' busy cycles
-// a vector instruction goes on (unpacking, the softmax of 16 columns), in a fifth or less a
-// matrix one.  Pieces of prompts (128 queries, four groups, 55 us) read little and spend as
-// large a share on vector instructions; 256 dimensions of 8 bits only a third, with one
-// wave per SIMD to cover the waits (18.6 us and 4.0 for 64 MB).
+// Measured (traced kernels, three inputs in turn; one MI355X).  One request of 131071 tokens,
+// 64/8 heads of 128, 4 bits, 143 MB: 33.0 us and 5.3 of the join, 4.3 TB/s, where a streaming
+// read has 6.2; 64 ragged ones up to 16384, 32/8 heads, 600 MB: 132 and 5.4 (118 for both
+// where calls follow one another); 16 ragged ones up to 8192, 64/8 heads, two groups: 24.4
+// and 4.6.  Memory and the vector units bound them together: in 67 to 78% of the SIMDs' busy
+// cycles a vector instruction goes on (unpacking, the softmax of 16 columns), in a fifth or
+// less a matrix one.  Pieces of prompts (128 queries, four groups, 55 us) read little and
+// spend as large a share on vector instructions; 256 dimensions of 8 bits only a third, with
+// one wave per SIMD to cover the waits (18.9 us and 4.4 for 57 MB).
 #pragma once
 
 #include <hip/hip_fp16.h>

@@ -33,18 +33,21 @@ int in_item(const seedlm_qcache_attend_args& a) { return std::min(shared_of(a), 
 // another, but the sums, the partials and the second launch (4 to 5 us) fall away.  That
 // pays up to so many steps, and up to twice as many where items fill half the chip.  Time
 // of a call, unsplit against split, lengths alike: one request of 8 cache heads and 128
-// dimensions, 4 bits, 8.4 and 10.1 us at 512 tokens, 10.1 and 10.1 at 768, 11.9 and 10.1
-// at 1024; 16 requests 12.6 and 13.9 at 1024, 16.3 and 16.8 at 1536, 19.9 and 17.5 at
-// 2048; 4 of 2 heads and 256 dimensions, 8 bits, 11.8 and 12.9 at 384, 13.2 and 13.0 at
-// 512; 8 of 32 heads and 64 dimensions, 8 bits, fp32, 11.5 and 16.0 at 1024, 17.8 and 20.3
-// at 2048, and 17.5 and 16.5 where they are ragged up to 2047.  With two workgroups for
-// every compute unit runs of even length gain nothing until lengths differ much: 64
-// requests 31.6 and 38.9 at 2048.  Items of several queries are as long as their
-// neighbours: 128 queries of one request of 2048 tokens (256 workgroups) 21.5 and 25.6,
-// 512 of 2048 46.6 and 56.5, 512 of 8192 159 and 164.  That holds from twice as many queries
-// of a row as an item takes (4 of 128 in a table of 64 rows 42.0 and 49.0); with fewer the
+// dimensions, 4 bits, 8.3 and 9.8 us at 512 tokens, 10.1 and 9.8 at 768, 11.9 and 9.9
+// at 1024; 16 requests 12.7 and 14.1 at 1024, 16.3 and 16.8 at 1536, 19.8 and 17.7 at
+// 2048; 4 of 2 heads and 256 dimensions, 8 bits, 10.5 and 11.9 at 384, 12.0 and 11.9 at
+// 512.  Lengths that differ shift the balance, since a call is as long as its longest item
+// and the runs share the sum: 16 requests ragged up to 1536 16.3 and 14.5.  64 dimensions
+// could go on past their 14 steps (1792 tokens) where lengths are alike (8 requests of 32
+// heads, 8 bits, 15.7 and 20.8 at 2048), not where they are ragged, as requests that are
+// served are (15.5 and 15.6; 4 requests 15.3 and 14.0; in fp32 17.5 and 16.5).  With two
+// workgroups for every compute unit runs of even length gain nothing until lengths differ
+// much: 64 requests 31.8 and 36.4 at 2048.  Items of several queries are as long as their
+// neighbours: 128 queries of one request of 2048 tokens (256 workgroups) 22.4 and 27.7,
+// 512 of 2048 48.7 and 58.7, 512 of 8192 167 and 175.  That holds from twice as many queries
+// of a row as an item takes (4 of 128 in a table of 64 rows 42.2 and 48.9); with fewer the
 // items may be single tokens of requests that have nothing in common (64 rows of 8 queries,
-// ragged up to 8000, 136 and 120, but 128 of 4000 124 and 129).
+// ragged up to 8000, 135 and 118, but 128 of 4000 125 and 131).
 bool unsplit(const seedlm_qcache_attend_args& a) {
   const int64_t items = (a.queries + in_item(a) - 1) / in_item(a);
   const int64_t workgroups = items * a.cache.kv_heads * qtiles_of(a);
