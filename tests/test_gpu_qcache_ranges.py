@@ -215,3 +215,32 @@ def test_weights_are_not_low_on_average(dim, bits, groups):
         error = np.where(value > 0, got / value - 1, 0.0).sum(2) / (value > 0).sum(2)
     assert np.abs(error).max() <= 2.0 ** -21
     assert abs(error.mean()) < 2.0 ** -25, error.mean()
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("dim,bits,groups", [f for f in FORMS if f[2] > 1])
+@pytest.mark.parametrize("pair", [(np.nan, 0), (np.inf, 0), (1, np.inf), (1, -np.inf)])
+def test_pairs_that_are_not_finite_beside_scales_far_apart(pair, dim, bits, groups, f16):
+    # a token's first group is not finite; its last has a scale far above all others', or below
+    import torch
+
+    lens = [200, 33, 1, 700]
+    x = make([dim, groups, 6], lens, 8, 2, dim, 16, f16, bits, groups)
+    tokens = [(0, 150), (1, 32), (2, 0), (3, 1), (3, 600)]
+    for power in (10, -10):
+        for b, n in enumerate(lens):
+            s = np.full((n, 2, groups), 2.0 ** -4)
+            for r, t in tokens:
+                if r == b:
+                    s[t, :, -1] = 2.0 ** power
+            values_of(x, b, s)
+        clean = [run(y) for y in (x, widen(x, 9000))]
+        for r, t in tokens:
+            page, row = x["where"][r][t]
+            x["cache"][3][page, row, :, 0] = torch.tensor(pair, dtype=torch.float16)
+        for y, was in zip((x, widen(x, 9000)), clean):
+            check(y, was)
+            got = run(y)
+            assert not np.isfinite(got[..., : dim // groups]).any()
+            got[..., : dim // groups] = was[..., : dim // groups]
+            check(y, got)
